@@ -441,6 +441,99 @@ AMK_API int amk_decode_step_noalloc(const amk_plan *plan, const amk_weights *w, 
                                     int32_t token_id, int32_t pos, float *logits_dev,
                                     int32_t *argmax_host, void *cuda_stream);
 
+/* ---- operators of the multi-token step --------------------------------- */
+/* (No counterpart in the AutoMegaKernel pages, which decode one token per
+ * launch: what a caller needs next to that step.)  The matrix product, the
+ * attention and the token choice that a step over several tokens is made of,
+ * each on caller-owned device memory.  amk_extend (below) runs a handle's
+ * model with the first two.  They take no handle, allocate nothing, keep
+ * nothing between calls, only enqueue work on cuda_stream (which may be
+ * capturing a CUDA graph; the graph then holds the arguments' pointers), and
+ * may be called from any host thread.  Pointers are device pointers of the
+ * current device, aligned to their element size unless more is said; inputs
+ * are only read.  A count of 0 (rows, tokens) is AMK_OK with nothing
+ * enqueued.  AMK_ERR_INVALID_ARG on a bad argument, AMK_ERR_NO_DEVICE without
+ * a device, AMK_ERR_CUDA if a launch fails. */
+
+/* y = act(x w^T + bias) [* (x up^T + up_bias)] [+ residual]: a matrix product
+ * with its epilogue; with `up` the gated pair of projections of an FFN.
+ * x is bf16 [m][k], w and up are in one of the model's weight formats with
+ * their scales (see amk_weights; rows contiguous, 1 <= n, k; an even k for
+ * W4A16), the biases bf16 [n] or NULL.  y and residual (or NULL) are [m][n] in
+ * bf16 or fp32, each with its own row stride; residual may be y itself (same
+ * pointer, stride and type), otherwise y overlaps no input.  Row strides are
+ * in elements and at least the row length.  Sums are fp32 and rounded once,
+ * to y's type.  x rows, w rows and their bases at multiples of 16 bytes run
+ * on the tensor cores' fast path; any others are taken by a slower kernel. */
+typedef enum { AMK_DT_BF16 = 0, AMK_DT_F32 = 1 } amk_dtype;
+typedef enum { AMK_ACT_NONE = 0, AMK_ACT_SILU = 1, AMK_ACT_GELU = 2 /* x Phi(x), exact */,
+               AMK_ACT_RELU = 3 } amk_act;
+typedef struct {
+    const void *x, *w, *w_scale, *bias, *up, *up_scale, *up_bias, *residual;
+    void *y;
+    int64_t ldx, ldr, ldy;            /* row strides of x, residual, y (elements) */
+    int32_t m, n, k;
+    int32_t quant;                    /* amk_quant of w and up */
+    int32_t act;                      /* amk_act */
+    int32_t residual_type, y_type;    /* amk_dtype */
+} amk_linear_args;
+AMK_API int amk_linear(const amk_linear_args *a, void *cuda_stream);
+
+/* Causal attention of n_tokens query tokens at positions pos .. pos +
+ * n_tokens - 1 over KV-cache rows (row j holds position j):
+ *   out[t][h] = sum_j softmax_j(scale q[t][h] . k[h / G][j]) v[h / G][j],
+ * G = n_heads / n_kv_heads, over the rows j <= p = pos + t that are within
+ * the window (j > p - window) or among the first `sinks` rows; window 0 = no
+ * window.  Every token sees at least its own row.  Rows that no token sees
+ * are never part of a result, whatever they hold (NaN included).
+ * All tensors bf16 with contiguous head_dim (1 .. 256); strides in elements.
+ * k and v have kv_rows >= pos + n_tokens rows per head; the blocks of
+ * amk_get_kv have head stride max_ctx * head_dim and row stride head_dim.
+ * scale 0 = 1 / sqrt(head_dim).  Softmax statistics and sums are fp32. */
+typedef struct {
+    const void *q, *k, *v;            /* [t][h][d], [kv head][row][d] */
+    void *out;                        /* [t][h][d] */
+    int64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride;
+    int64_t k_head_stride, k_row_stride, v_head_stride, v_row_stride;
+    int32_t n_tokens, pos, n_heads, n_kv_heads, head_dim, kv_rows, window, sinks;
+    float scale;
+} amk_attention_args;
+AMK_API int amk_attention(const amk_attention_args *a, void *cuda_stream);
+
+/* Verification of n_draft drafted tokens against the target's distributions,
+ * from given random numbers (speculative sampling).  p_i = softmax(target[i]
+ * / temperature) for i = 0 .. n_draft, q_i = softmax(draft[i] / temperature)
+ * for i < n_draft, or, with draft NULL, all of q_i on draft_tokens[i].
+ * In order, token i is accepted when u[i] q_i(token) < p_i(token).  At the
+ * first one that is not, the next token is drawn from max(p_i - q_i, 0) (from
+ * p_i where that is 0 everywhere), after n_draft accepted ones from
+ * p_n_draft: the lowest token whose cumulative weight passes u[n_draft] times
+ * the total.  So each token is distributed as the target's, and n_draft = 0
+ * samples one.  temperature 0 is greedy: a token is accepted when it is the
+ * target's largest logit (lowest index), which is also what is drawn.
+ *  target:  fp32 [n_draft + 1][vocab], draft: fp32 [n_draft][vocab]; row
+ *           strides in elements; -inf is a token of probability 0.
+ *  u:       fp32 [n_draft + 1] in [0, 1).
+ *  tokens:  int32 [n_draft + 1]: the accepted tokens, the drawn one, then -1.
+ *  n_accepted: int32 [1].
+ * A drafted token outside [0, vocab) is not accepted.  A row that is reached
+ * and holds NaN or +inf, or nothing but -inf, has no distribution: nothing is
+ * accepted or drawn there (its token is -1).  n_draft <= 64. */
+typedef struct {
+    const float *target, *draft, *u;
+    const int32_t *draft_tokens;
+    int32_t *tokens, *n_accepted;
+    int64_t target_stride, draft_stride;
+    int32_t n_draft, vocab;
+    float temperature;      /* 0, or 1e-6 .. 1e6 */
+    void *workspace;        /* 16-byte aligned; its contents need not be kept */
+    int64_t workspace_bytes;
+} amk_verify_args;
+/* Bytes of workspace that a call needs (negative: a bad argument).  Calls that
+ * can overlap on the GPU need workspaces of their own. */
+AMK_API int64_t amk_verify_workspace(int32_t n_draft, int32_t vocab);
+AMK_API int amk_verify_draft(const amk_verify_args *a, void *cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -13,7 +13,8 @@ from typing import Dict, List, Optional, Tuple
 from . import abi
 
 __all__ = ["AmkError", "Decoder", "Plan", "validate_graph", "default_options", "version",
-           "make_config", "weights_struct", "decode_step_noalloc", "read_ceiling"]
+           "make_config", "weights_struct", "decode_step_noalloc", "read_ceiling",
+           "linear", "attention", "verify_draft"]
 
 
 class AmkError(RuntimeError):
@@ -378,3 +379,6 @@ class Decoder:
             self.close()
         except Exception:
             pass
+
+
+from .ops import attention, linear, verify_draft  # noqa: E402  (they use AmkError and _check)

@@ -21,6 +21,8 @@ STATUS = {
 }
 ERR = {v: k for k, v in STATUS.items()}
 QUANT_BF16, QUANT_W8A16, QUANT_W4A16 = 0, 1, 2
+DT_BF16, DT_F32 = 0, 1
+ACT = {"none": 0, "silu": 1, "gelu": 2, "relu": 3}
 ACC_READ, ACC_WRITE, ACC_ACCUM, ACC_READ_PREV, ACC_RESET, ACC_READ_FLAGGED = range(6)
 BUF_OUTPUT = 1
 RULES = {0: "ok", 1: "V1", 2: "V2", 3: "V3", 4: "V4", 5: "V5", 6: "V6", 7: "V7",
@@ -102,6 +104,31 @@ class Workspace(ctypes.Structure):
                 ("qkv_rows", c_i32)]
 
 
+class LinearArgs(ctypes.Structure):
+    _fields_ = [(n, c_vp) for n in ("x", "w", "w_scale", "bias", "up", "up_scale", "up_bias",
+                                    "residual", "y")] + [
+        ("ldx", c_i64), ("ldr", c_i64), ("ldy", c_i64), ("m", c_i32), ("n", c_i32),
+        ("k", c_i32), ("quant", c_i32), ("act", c_i32), ("residual_type", c_i32),
+        ("y_type", c_i32)]
+
+
+class AttentionArgs(ctypes.Structure):
+    _fields_ = [(n, c_vp) for n in ("q", "k", "v", "out")] + [
+        (n, c_i64) for n in ("q_token_stride", "q_head_stride", "out_token_stride",
+                             "out_head_stride", "k_head_stride", "k_row_stride",
+                             "v_head_stride", "v_row_stride")] + [
+        (n, c_i32) for n in ("n_tokens", "pos", "n_heads", "n_kv_heads", "head_dim", "kv_rows",
+                             "window", "sinks")] + [("scale", c_f32)]
+
+
+class VerifyArgs(ctypes.Structure):
+    _fields_ = [(n, c_vp) for n in ("target", "draft", "u", "draft_tokens", "tokens",
+                                    "n_accepted")] + [
+        ("target_stride", c_i64), ("draft_stride", c_i64), ("n_draft", c_i32),
+        ("vocab", c_i32), ("temperature", c_f32), ("workspace", c_vp),
+        ("workspace_bytes", c_i64)]
+
+
 # every function include/amk.h declares: name -> (restype, argtypes)
 SIGNATURES = {
     "amk_version": (ctypes.c_char_p, []),
@@ -134,6 +161,10 @@ SIGNATURES = {
                                         ctypes.POINTER(ctypes.c_double)]),
     "amk_decode_step_noalloc": (ctypes.c_int, [c_vp, ctypes.POINTER(Weights), c_vp, c_i32,
                                                c_i32, c_vp, ctypes.POINTER(c_i32), c_vp]),
+    "amk_linear": (ctypes.c_int, [ctypes.POINTER(LinearArgs), c_vp]),
+    "amk_attention": (ctypes.c_int, [ctypes.POINTER(AttentionArgs), c_vp]),
+    "amk_verify_workspace": (c_i64, [c_i32, c_i32]),
+    "amk_verify_draft": (ctypes.c_int, [ctypes.POINTER(VerifyArgs), c_vp]),
 }
 
 _LIB = None
