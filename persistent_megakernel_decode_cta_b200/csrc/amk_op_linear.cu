@@ -1,71 +1,15 @@
-// amk_op_linear.cu -- amk_linear: the matrix product with its epilogue.
-#include <cuda_fp16.h>
+// amk_op_linear.cu -- amk_linear: argument checks, the choice of a kernel, and
+// the kernel for any alignment.
+#include <atomic>
 #include <math.h>
 
-#include "amk_ops.h"
+#include "amk_op_linear.cuh"
 
 namespace amk {
+namespace linear {
 namespace {
 
 constexpr int kQ4GroupLog2 = 7;
-
-__device__ __forceinline__ float bf16f(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
-// round to nearest even; the cast of a NaN stays a NaN
-__device__ __forceinline__ uint16_t f_bf16(float f)
-{
-    uint16_t r;
-    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(f));
-    return r;
-}
-
-// The epilogue of one output: act(a + bias) [* (u + up_bias)] [+ residual].
-struct Epilogue {
-    const uint16_t *bias, *up_bias;
-    const uint16_t *w_scale, *up_scale;  // fp16 row scales (W8A16), or null
-    const void *residual;
-    void *y;
-    int64_t ldr, ldy;
-    int32_t m, n, act, gated, res_f32, y_f32;
-};
-
-__device__ __forceinline__ float activate(int act, float v)
-{
-    if (act == AMK_ACT_SILU)
-        return v / (1.f + __expf(-v));
-    if (act == AMK_ACT_GELU)
-        return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
-    if (act == AMK_ACT_RELU)
-        return v < 0.f ? 0.f : v;  // a NaN stays
-    return v;
-}
-
-__device__ __forceinline__ void store_out(const Epilogue &e, int row, int col, float a, float u)
-{
-    if (row >= e.m || col >= e.n)
-        return;
-    if (e.w_scale)
-        a *= __half2float(__ushort_as_half(e.w_scale[col]));
-    if (e.bias)
-        a += bf16f(e.bias[col]);
-    a = activate(e.act, a);
-    if (e.gated) {
-        if (e.up_scale)
-            u *= __half2float(__ushort_as_half(e.up_scale[col]));
-        if (e.up_bias)
-            u += bf16f(e.up_bias[col]);
-        a *= u;
-    }
-    if (e.residual) {
-        const int64_t i = row * e.ldr + col;
-        a += e.res_f32 ? static_cast<const float *>(e.residual)[i]
-                       : bf16f(static_cast<const uint16_t *>(e.residual)[i]);
-    }
-    const int64_t o = row * e.ldy + col;
-    if (e.y_f32)
-        static_cast<float *>(e.y)[o] = a;
-    else
-        static_cast<uint16_t *>(e.y)[o] = f_bf16(a);
-}
 
 // ---- the kernel for any alignment ---------------------------------------------
 // A 64 x 64 tile of y per CTA, K in blocks of 32, bf16 mma.sync with fp32
@@ -178,8 +122,7 @@ __global__ void __launch_bounds__(128) linear_generic(const GenericParams p)
                             for (int c = 0; c < 2; ++c) {
                                 const int n = n0 + wn + j * 8 + 2 * t + c;
                                 const float s =
-                                    n < p.e.n ? __half2float(__ushort_as_half(
-                                                    (b ? p.up_gs : p.w_gs)[(int64_t)n * p.groups + grp]))
+                                    n < p.e.n ? fp16f((b ? p.up_gs : p.w_gs)[(int64_t)n * p.groups + grp])
                                               : 0.f;
 #pragma unroll
                                 for (int i = 0; i < 2; ++i)
@@ -198,9 +141,13 @@ __global__ void __launch_bounds__(128) linear_generic(const GenericParams p)
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    store_out(p.e, m0 + wm + i * 16 + g + (r >> 1) * 8,
-                              n0 + wn + j * 8 + 2 * t + (r & 1), acc[0][i][j][r],
-                              MATS == 2 ? acc[MATS - 1][i][j][r] : 0.f);
+                {
+                    const int m = m0 + wm + i * 16 + g + (r >> 1) * 8;
+                    const int n = n0 + wn + j * 8 + 2 * t + (r & 1);
+                    if (m < p.e.m && n < p.e.n)
+                        emit(p.e, row_const(p.e, n), m, n, acc[0][i][j][r],
+                             MATS == 2 ? acc[MATS - 1][i][j][r] : 0.f);
+                }
     }
 }
 
@@ -251,12 +198,177 @@ int check_linear(const amk_linear_args *a)
     return AMK_OK;
 }
 
+// ---- the tensor-core kernel ----------------------------------------------------
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                 const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                 const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_fn()
+{
+    static std::atomic<EncodeTiled> fn{nullptr};
+    EncodeTiled f = fn.load(std::memory_order_relaxed);
+    if (!f) {
+        void *sym = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &sym, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess) {
+            f = reinterpret_cast<EncodeTiled>(sym);
+            fn.store(f, std::memory_order_relaxed);
+        }
+        cudaGetLastError();
+    }
+    return f;
+}
+
+// Map of `rows` rows of `inner` elements, `pitch` bytes apart, in boxes of
+// box_inner x box_rows.
+bool encode(CUtensorMap *map, CUtensorMapDataType type, const void *base, int64_t inner,
+            int64_t rows, int64_t pitch, int box_inner, int box_rows, CUtensorMapSwizzle swizzle)
+{
+    const EncodeTiled f = encode_fn();
+    const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)pitch};
+    const cuuint32_t box[2] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows}, one[2] = {1, 1};
+    return f && f(map, type, 2, const_cast<void *>(base), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int sm_count()
+{
+    static std::atomic<int> sms[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+        return 0;
+    n = sms[dev].load(std::memory_order_relaxed);
+    if (!n && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
+        sms[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+bool fits_tensor_cores(const amk_linear_args *a)
+{
+    const int64_t row = a->quant == AMK_QUANT_BF16    ? 2 * (int64_t)a->k
+                        : a->quant == AMK_QUANT_W8A16 ? a->k
+                        : a->k % 2                    ? 1
+                                                      : a->k / 2;
+    return aligned(a->x, 16) && aligned(a->w, 16) && aligned(a->up, 16) && row % 16 == 0 &&
+           (a->m == 1 || a->ldx % 8 == 0);
+}
+
+// The variant, the CTAs of a cluster that share a tile, and the grid.
+struct Choice {
+    Variant v;
+    int split, grid;
+};
+
+Choice choose(const amk_linear_args *a, int sms)
+{
+    const int rows = a->up ? 64 : 128;
+    const int64_t tn = ((int64_t)a->n + rows - 1) / rows;
+    const bool codes = a->quant != AMK_QUANT_BF16;
+    Choice best{};
+    double cost = 1e300;
+    // Cycles of the tiles that one SM runs one after the other: 64 inputs of a
+    // tile of nt tokens take 2 nt of them on the tensor cores (but the weights'
+    // 16 KB no less than 400 from HBM), a tile's start and end some thousands.
+    const int blocks64 = (a->k + 63) / 64;
+    for (int nt : {16, 32, 64, 128}) {
+        const int64_t tiles = tn * (((int64_t)a->m + nt - 1) / nt);
+        if (nt > 16 && a->m <= nt / 2)
+            continue;
+        const int per_sm = nt <= 64 ? 2 : 1;
+        for (int split = 1; split <= 8 && split <= (a->k + 127) / 128; split *= 2) {
+            const int64_t waves = (tiles * split + (int64_t)sms * per_sm - 1) / (sms * per_sm);
+            const double block = (2.0 * nt > 400 ? 2.0 * nt : 400) * per_sm;
+            const double c = waves * ((double)((blocks64 + split - 1) / split) * block + 4000 +
+                                      300 * split);
+            if (c < cost && tiles * split <= INT32_MAX) {
+                cost = c;
+                best.v = {nt, true, true};
+                best.split = split;
+                best.grid = (int)(tiles * split);
+            }
+        }
+    }
+    {
+        const bool promote = a->y_type == AMK_DT_F32 || a->quant == AMK_QUANT_W4A16;
+        const int nt = codes && promote ? 128 : 256;
+        const int64_t tiles = tn * (((int64_t)a->m + nt - 1) / nt);
+        const int64_t waves = (tiles + sms - 1) / sms;
+        const double c = waves * ((double)blocks64 * 2.0 * nt) + 5000;
+        if (c < cost && tiles <= INT32_MAX) {
+            best.v = {nt, false, promote};
+            best.split = 1;
+            best.grid = (int)(tiles < sms ? tiles : sms);
+        }
+    }
+    return best;
+}
+
+int launch_tc(const amk_linear_args *a, const Epilogue &e, cudaStream_t stream)
+{
+    const int sms = sm_count();
+    if (!sms) {
+        int n = 0;
+        const cudaError_t err = cudaGetDeviceCount(&n);
+        return launch_status(err == cudaSuccess ? cudaErrorNoDevice : err, "amk_linear");
+    }
+    const Choice c = choose(a, sms);
+    TcParams p;
+    p.e = e;
+    const int ksub = a->quant == AMK_QUANT_W4A16 || c.v.split ? 2 : 1;
+    const int rows = a->up ? 64 : 128;
+    p.groups = (a->k + kQ4Group - 1) / kQ4Group;
+    p.w_gs = static_cast<const uint16_t *>(a->w_scale);
+    p.up_gs = static_cast<const uint16_t *>(a->up_scale);
+    p.blocks = (a->k + ksub * 64 - 1) / (ksub * 64);
+    // int4: a sum for each group of 128 inputs, to be scaled by itself; fp32
+    // outputs: 512 inputs; bf16 outputs round away more than is cut off
+    p.seg = a->quant == AMK_QUANT_W4A16 ? 1
+            : a->y_type == AMK_DT_F32   ? 8 / ksub
+                                        : p.blocks;
+    p.tiles_m = (int)(((int64_t)a->m + c.v.nt - 1) / c.v.nt);
+    p.tiles = (int)(((int64_t)a->n + rows - 1) / rows) * p.tiles_m;
+    p.split = c.split;
+    bool ok = encode(&p.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a->x, a->k, a->m,
+                     a->m == 1 ? (2 * (int64_t)a->k + 15) & ~(int64_t)15 : 2 * a->ldx, 64, c.v.nt,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+    for (int i = 0; i < (a->up ? 2 : 1) && ok; ++i) {
+        CUtensorMap *map = i ? &p.up : &p.w;
+        const void *w = i ? a->up : a->w;
+        if (a->quant == AMK_QUANT_BF16)
+            ok = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, w, a->k, a->n, 2 * (int64_t)a->k, 64,
+                        rows, CU_TENSOR_MAP_SWIZZLE_128B);
+        else {
+            const int per = a->quant == AMK_QUANT_W8A16 ? 1 : 2;  // codes to a byte
+            ok = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, a->k / per, a->n, a->k / per,
+                        ksub * 64 / per, rows, CU_TENSOR_MAP_SWIZZLE_NONE);
+        }
+    }
+    if (!ok)
+        return amk_set_error(AMK_ERR_CUDA, "amk_linear: a tensor map was refused");
+    cudaError_t err;
+    if (a->quant == AMK_QUANT_W8A16)
+        err = launch_int8(c.v, p, c.grid, stream);
+    else if (a->quant == AMK_QUANT_W4A16)
+        err = launch_int4(c.v, p, c.grid, stream);
+    else
+        err = launch_bf16(c.v, p, c.grid, stream);
+    return launch_status(err, "amk_linear");
+}
+
 }  // namespace
+}  // namespace linear
 }  // namespace amk
 
 extern "C" int amk_linear(const amk_linear_args *a, void *cuda_stream)
 {
     using namespace amk;
+    using namespace amk::linear;
     const int rc = check_linear(a);
     if (rc != AMK_OK || a->m == 0)
         return rc;
@@ -287,6 +399,8 @@ extern "C" int amk_linear(const amk_linear_args *a, void *cuda_stream)
     p.e.res_f32 = a->residual_type == AMK_DT_F32;
     p.e.y_f32 = a->y_type == AMK_DT_F32;
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+    if (fits_tensor_cores(a))
+        return launch_tc(a, p.e, st);
     cudaError_t e;
     if (a->quant == AMK_QUANT_W8A16)
         e = launch_generic<AMK_QUANT_W8A16>(p, st);

@@ -1,0 +1,566 @@
+// amk_op_linear.cuh -- the tensor-core kernel of amk_linear, and the epilogue
+// that it shares with the kernel for any alignment.
+//
+// y = x w^T is taken as its transpose: the 128 rows of the tcgen05 tile are
+// rows of w (or 64 of w and 64 of up), its NT columns are tokens.  So the
+// tile has 128 rows however few tokens there are, the weights stream through
+// shared memory once for up to NT tokens, and a thread of the epilogue holds
+// one row of w: its scale and bias are two registers, and a warp's stores of a
+// token are 32 consecutive outputs.
+//
+// Warps: 0 fetches K blocks with TMA into a ring of stages, 1 issues the MMAs,
+// 2 owns the TMEM, 4.. drain the accumulators (two buffers, so that the next
+// sum runs meanwhile); with int8 and int4 weights four more turn the codes into
+// the bf16 integers they are (exact) in the layout the MMA reads.  int8 row
+// scales are applied to the sums.  The sums of an int4 row's 128-input groups
+// are scaled apart: each group is a sum of its own (`seg`), which the draining
+// warps scale and add in fp32 registers.  So weights are never rounded.
+//
+// Tensor cores cut off what falls below their accumulators when they align
+// the terms of a sum, always downward in magnitude: over K = 4096 an fp32
+// output lost 3e-6 of its size.  fp32 outputs are therefore summed in segments
+// too (`promote`).
+#ifndef AMK_OP_LINEAR_CUH
+#define AMK_OP_LINEAR_CUH
+
+#include "amk_op_linear.h"
+#include "amk_ops.cuh"
+
+namespace amk {
+namespace linear {
+namespace {
+
+using namespace ops;
+
+__device__ __forceinline__ float activate(int act, float v)
+{
+    if (act == AMK_ACT_SILU)
+        return v / (1.f + __expf(-v));
+    if (act == AMK_ACT_GELU)
+        return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
+    if (act == AMK_ACT_RELU)
+        return v < 0.f ? 0.f : v;  // a NaN stays
+    return v;
+}
+
+// What an output row of w brings to the epilogue: scales and biases.
+struct RowConst {
+    float ws, bias, us, ubias;
+};
+__device__ __forceinline__ RowConst row_const(const Epilogue &e, int n)
+{
+    RowConst c = {1.f, 0.f, 1.f, 0.f};
+    if (n < e.n) {
+        if (e.w_scale)
+            c.ws = fp16f(e.w_scale[n]);
+        if (e.bias)
+            c.bias = bf16f(e.bias[n]);
+        if (e.up_scale)
+            c.us = fp16f(e.up_scale[n]);
+        if (e.up_bias)
+            c.ubias = bf16f(e.up_bias[n]);
+    }
+    return c;
+}
+__device__ __forceinline__ float residual_at(const Epilogue &e, int64_t m, int n)
+{
+    return e.res_f32 ? static_cast<const float *>(e.residual)[m * e.ldr + n]
+                     : bf16f(static_cast<const uint16_t *>(e.residual)[m * e.ldr + n]);
+}
+__device__ __forceinline__ void store_at(const Epilogue &e, int64_t m, int n, float v)
+{
+    if (e.y_f32)
+        static_cast<float *>(e.y)[m * e.ldy + n] = v;
+    else
+        static_cast<uint16_t *>(e.y)[m * e.ldy + n] = f_bf16(v);
+}
+// One output from its sums.
+__device__ __forceinline__ void emit(const Epilogue &e, const RowConst &c, int m, int n, float a,
+                                     float u)
+{
+    float v = activate(e.act, fmaf(a, c.ws, c.bias));
+    if (e.gated)
+        v *= fmaf(u, c.us, c.ubias);
+    if (e.residual)
+        v += residual_at(e, m, n);
+    store_at(e, m, n, v);
+}
+
+// Exact bf16 pairs of int8 codes: 128 + the low seven bits, less 256 or 128 by
+// the sign.  w holds the codes in the low bytes of its halves.
+__device__ __forceinline__ uint32_t i8_pair(uint32_t w)
+{
+    const uint32_t a = (w & 0x007f007fu) | 0x43004300u, s = (w & 0x00800080u) | 0x43004300u;
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(s));
+    return r;
+}
+// Exact bf16 pairs of int4 codes in the low nibbles of the halves: 128 + (code
+// + 8), less 136.
+__device__ __forceinline__ uint32_t i4_pair(uint32_t w)
+{
+    const uint32_t a = (w & 0x000f000fu) ^ 0x43084308u;
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x43084308u));
+    return r;
+}
+
+template <int QUANT, int NT, bool SPLIT, bool PROMOTE>
+struct Cfg {
+    // K elements of a stage, in blocks of 64 (one swizzled row of bf16): two
+    // for int4 (rows of 64 bytes) and where the weights only stream through
+    static constexpr int KSUB = QUANT == AMK_QUANT_W4A16 || SPLIT ? 2 : 1;
+    static constexpr int BLK = 128 * 128;  // a block of 128 rows of 64 bf16
+    static constexpr int A = KSUB * BLK, X = KSUB * NT * 128;
+    static constexpr int RAW = QUANT == AMK_QUANT_W8A16   ? KSUB * 64 * 128
+                               : QUANT == AMK_QUANT_W4A16 ? KSUB * 32 * 128
+                                                          : 0;
+    static constexpr int STAGE = X + (RAW ? RAW : A);
+    static constexpr int ASTAGES = RAW ? 2 : 0;  // converted blocks
+    static constexpr int XCH = SPLIT ? 0 : 2 * 2 * 16 * 64 * 4;
+    // of an SM's 227 KB: half for a CTA where weights stream (two CTAs to an SM
+    // keep the stream going while one starts or ends), else all of it
+    static constexpr int ROOM = (SPLIT && NT <= 64 ? 112 * 1024 : 224 * 1024) - 2048 - XCH;
+    static constexpr int FIT = (ROOM - ASTAGES * BLK) / STAGE;
+    static constexpr int STAGES = FIT > 8 ? 8 : FIT;
+    static constexpr int SMEM = STAGES * STAGE + ASTAGES * BLK + XCH + 1024;
+    static constexpr int EW = NT >= 64 ? 2 : 1;  // draining warpgroups
+    static constexpr int NC = NT / EW;           // columns of each
+    static constexpr int THREADS = 128 + EW * 128 + (RAW ? 128 : 0);
+    static constexpr int CTAS = SPLIT && NT <= 64 ? 2 : 1;  // to an SM
+    static constexpr int COLS = 2 * NT < 32 ? 32 : 2 * NT;  // TMEM columns
+    static_assert(STAGES >= 2, "a ring needs two stages");
+    static_assert(!SPLIT || NT * 512 <= STAGES * STAGE + ASTAGES * BLK, "the sums reuse the ring");
+};
+
+__device__ unsigned int g_timeouts;  // CTAs that gave up a wait
+
+template <int QUANT, int NT, bool SPLIT, bool PROMOTE>
+__global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
+                                  Cfg<QUANT, NT, SPLIT, PROMOTE>::CTAS)
+    linear_tc(const __grid_constant__ TcParams p)
+{
+    using C = Cfg<QUANT, NT, SPLIT, PROMOTE>;
+    constexpr bool CODES = QUANT != AMK_QUANT_BF16;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[2 * C::STAGES + 2 * 2 + 4];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int fail_flag;
+    volatile int *fail = &fail_flag;
+    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t abuf = ring + C::STAGES * C::STAGE;  // converted blocks
+    const uint32_t xch = abuf + C::ASTAGES * C::BLK;
+    const uint32_t bar0 = smem_u32(bars);
+    auto full = [&](int s) { return bar0 + 8 * s; };
+    auto empty = [&](int s) { return bar0 + 8 * (C::STAGES + s); };
+    auto afull = [&](int s) { return bar0 + 8 * (2 * C::STAGES + s); };
+    auto aempty = [&](int s) { return bar0 + 8 * (2 * C::STAGES + 2 + s); };
+    auto accf = [&](int b) { return bar0 + 8 * (2 * C::STAGES + 4 + b); };
+    auto acce = [&](int b) { return bar0 + 8 * (2 * C::STAGES + 6 + b); };
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        fail_flag = 0;
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), CODES ? 5 : 1);  // the MMAs, and the four converting warps
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(afull(s), 4);
+            mbar_init(aempty(s), 1);
+            mbar_init(accf(s), 1);
+            mbar_init(acce(s), 4 * C::EW);
+        }
+        mbar_init_fence();
+        prefetch_map(&p.x);
+        prefetch_map(&p.w);
+        if (p.e.gated)
+            prefetch_map(&p.up);
+    }
+    if (warp == 2)
+        tmem_alloc<C::COLS>(smem_u32(&tmem_slot));
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const bool gated = p.e.gated;
+    const int rows_out = gated ? 64 : 128;
+    const int split = SPLIT ? p.split : 1, rank = SPLIT ? (int)(blockIdx.x % split) : 0;
+    const int first = SPLIT ? blockIdx.x / split : blockIdx.x;
+    const int step = SPLIT ? p.tiles : gridDim.x;  // a split tile is the cluster's only one
+    const int kb0 = (int)((int64_t)p.blocks * rank / split);
+    const int kb1 = (int)((int64_t)p.blocks * (rank + 1) / split);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int tile = first; tile < p.tiles && ok; tile += step) {
+                const int n0 = (tile / p.tiles_m) * rows_out, m0 = (tile % p.tiles_m) * NT;
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const int s = it % C::STAGES;
+                    if (!mbar_wait(empty(s), ((it / C::STAGES) & 1) ^ 1, fail)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t xs = ring + s * C::STAGE, ws = xs + C::X;
+                    const int k = kb * C::KSUB * 64;
+                    mbar_expect_tx(full(s), C::STAGE);
+                    if (CODES) {
+                        const int kx = QUANT == AMK_QUANT_W8A16 ? k : k / 2;
+                        tma_2d(ws, &p.w, kx, n0, full(s));
+                        if (gated)
+                            tma_2d(ws + C::RAW / 2, &p.up, kx, n0, full(s));
+                    }
+#pragma unroll
+                    for (int j = 0; j < C::KSUB; ++j) {
+                        if (!CODES) {
+                            tma_2d(ws + j * 16384, &p.w, k + j * 64, n0, full(s));
+                            if (gated)
+                                tma_2d(ws + j * 16384 + 8192, &p.up, k + j * 64, n0, full(s));
+                        }
+                        tma_2d(xs + j * NT * 128, &p.x, k + j * 64, m0, full(s));
+                    }
+                }
+            }
+            if (!ok)  // no copy may land after the CTA has gone
+                for (uint32_t j = it > C::STAGES ? it - C::STAGES : 0; j < it; ++j) {
+                    const uint64_t t0 = gtimer();
+                    while (!mbar_try_wait(full(j % C::STAGES), (j / C::STAGES) & 1) &&
+                           gtimer() - t0 < 1000000000ull) {
+                    }
+                }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = tc_idesc(128, NT);
+            uint32_t it = 0, sc = 0;
+            bool ok = true;
+            for (int tile = first; tile < p.tiles && ok; tile += step) {
+                for (int kb = kb0; kb < kb1 && ok; ++sc) {
+                    const int b = sc & 1, end = min(kb + p.seg, kb1);
+                    if (!mbar_wait(acce(b), ((sc >> 1) & 1) ^ 1, fail)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    uint32_t accumulate = 0;
+                    for (; kb < end && ok; ++kb, ++it) {
+                        const int s = it % C::STAGES;
+                        if (!mbar_wait(full(s), (it / C::STAGES) & 1, fail)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t xs = ring + s * C::STAGE;
+#pragma unroll
+                        for (int j = 0; j < C::KSUB; ++j) {
+                            uint32_t ws = xs + C::X + j * C::BLK;
+                            if (CODES) {
+                                const uint32_t ci = it * C::KSUB + j;
+                                ws = abuf + (ci & 1) * C::BLK;
+                                if (!mbar_wait(afull(ci & 1), (ci >> 1) & 1, fail)) {
+                                    ok = false;
+                                    break;
+                                }
+                            }
+                            tc_fence_after();
+                            const uint64_t ad = tc_desc(ws), bd = tc_desc(xs + j * NT * 128);
+#pragma unroll
+                            for (int k16 = 0; k16 < 4; ++k16) {  // 32 bytes of a row each
+                                tc_mma(tmem + b * NT, ad + 2 * k16, bd + 2 * k16, idesc,
+                                       accumulate);
+                                accumulate = 1;
+                            }
+                            if (CODES)
+                                tc_commit(aempty((it * C::KSUB + j) & 1));
+                        }
+                        tc_commit(empty(s));
+                    }
+                    if (ok)
+                        tc_commit(accf(b));
+                }
+            }
+        }
+    } else if (warp >= 4 && warp < 4 + 4 * C::EW) {
+        const int wg = (warp - 4) >> 2, q = warp & 3, r = q * 32 + lane;  // row of the tile
+        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + wg * C::NC;
+        uint32_t sc = 0;
+        bool ok = true;
+        for (int tile = first; tile < p.tiles && ok; tile += step) {
+            const int n0 = (tile / p.tiles_m) * rows_out, m0 = (tile % p.tiles_m) * NT;
+            const bool is_up = gated && r >= 64;
+            const int n = n0 + (is_up ? r - 64 : r);
+            const uint16_t *gs = nullptr;  // the row's group scales
+            if (QUANT == AMK_QUANT_W4A16 && n < p.e.n)
+                gs = (is_up ? p.up_gs : p.w_gs) + (int64_t)n * p.groups;
+            float acc[PROMOTE ? C::NC : 1];
+            if constexpr (PROMOTE) {
+#pragma unroll
+                for (int c = 0; c < C::NC; ++c)
+                    acc[c] = 0.f;
+                uint16_t next = gs ? gs[kb0] : (uint16_t)0;  // seg = a group of 128 = a block
+                for (int kb = kb0; kb < kb1; kb += p.seg, ++sc) {
+                    const int b = sc & 1;
+                    float scale = 1.f;
+                    if (QUANT == AMK_QUANT_W4A16) {
+                        scale = fp16f(next);
+                        if (gs && kb + p.seg < kb1)
+                            next = gs[kb + p.seg];
+                    }
+                    if (!warp_wait(accf(b), (sc >> 1) & 1, fail)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int c0 = 0; c0 < C::NC; c0 += 16) {
+                        float v[16];
+                        tmem_ld16(taddr + b * NT + c0, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            acc[c0 + c] = QUANT == AMK_QUANT_W4A16
+                                              ? fmaf(v[c], scale, acc[c0 + c])
+                                              : acc[c0 + c] + v[c];
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(acce(b));
+                }
+            }
+            if (!ok)
+                break;
+            if constexpr (SPLIT) {
+                static_assert(PROMOTE, "a split tile's sums are held in registers");
+                // the ring is idle: every MMA that read it has finished
+#pragma unroll
+                for (int c = 0; c < C::NC; ++c)
+                    sts32f(ring + (uint32_t)((wg * C::NC + c) * 128 + r) * 4, acc[c]);
+            } else {
+                const int b = sc & 1;
+                if (!PROMOTE) {
+                    if (!warp_wait(accf(b), (sc >> 1) & 1, fail)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                }
+                const RowConst rc = row_const(p.e, n);
+                const int cols = min(C::NC, p.e.m - m0 - wg * C::NC);  // tokens there are
+#pragma unroll
+                for (int c0 = 0; c0 < C::NC; c0 += 16) {
+                    float v[16];
+                    if constexpr (PROMOTE) {
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            v[c] = acc[c0 + c];
+                    } else {
+                        tmem_ld16(taddr + b * NT + c0, v);
+                        tmem_ld_wait();
+                        if (c0 + 16 == C::NC) {  // the buffer has been read
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0)
+                                mbar_arrive(acce(b));
+                        }
+                    }
+                    if (c0 >= cols)
+                        continue;
+                    const int64_t mc = (int64_t)m0 + wg * C::NC + c0;
+                    const bool mine = n < p.e.n && !is_up;
+                    float res[16];
+                    if (p.e.residual) {
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            res[c] = mine && c0 + c < cols ? residual_at(p.e, mc + c, n) : 0.f;
+                    }
+                    // a gated row's other half sits 64 lanes on: through shared memory,
+                    // in two buffers by turns so that one barrier a round suffices
+                    const uint32_t xb =
+                        xch + (uint32_t)((wg * 2 + ((c0 >> 4) & 1)) * 16 * 64) * 4;
+                    if (gated) {
+                        if (is_up) {
+#pragma unroll
+                            for (int c = 0; c < 16; ++c)
+                                sts32f(xb + (uint32_t)(c * 64 + r - 64) * 4,
+                                       fmaf(v[c], rc.us, rc.ubias));
+                        }
+                        named_bar(1 + wg, 128);
+                    }
+                    if (mine) {
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            if (c0 + c < cols) {
+                                float o = activate(p.e.act, fmaf(v[c], rc.ws, rc.bias));
+                                if (gated)
+                                    o *= lds32f(xb + (uint32_t)(c * 64 + r) * 4);
+                                if (p.e.residual)
+                                    o += res[c];
+                                store_at(p.e, mc + c, n, o);
+                            }
+                        }
+                    }
+                }
+                if (gated)  // both buffers are read before the next tile writes them
+                    named_bar(1 + wg, 128);
+                if (!PROMOTE)
+                    ++sc;
+            }
+        }
+    } else if (CODES && warp >= 4 + 4 * C::EW) {
+        const int cw = warp - 4 - 4 * C::EW;  // converting warp 0 .. 3
+        uint32_t it = 0;
+        bool ok = true;
+        for (int tile = first; tile < p.tiles && ok; tile += step)
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const int s = it % C::STAGES;
+                if (!warp_wait(full(s), (it / C::STAGES) & 1, fail)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t src = ring + s * C::STAGE + C::X;
+                for (int j = 0; j < C::KSUB && ok; ++j) {
+                    const uint32_t ci = it * C::KSUB + j;
+                    if (!warp_wait(aempty(ci & 1), ((ci >> 1) & 1) ^ 1, fail)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t dst = abuf + (ci & 1) * C::BLK;
+                    if (QUANT == AMK_QUANT_W8A16) {
+                        // 16 codes at a time, four lanes to a row
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int row = cw * 32 + i * 8 + (lane >> 2), c = lane & 3;
+                            const uint4 v = lds128(src + row * (C::KSUB * 64) + j * 64 + c * 16);
+                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                            uint32_t o[8];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                o[2 * e] = i8_pair(__byte_perm(w[e], 0, 0x4140));
+                                o[2 * e + 1] = i8_pair(__byte_perm(w[e], 0, 0x4342));
+                            }
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                sts128(dst + row * 128 + (((2 * c + e) ^ (row & 7)) << 4),
+                                       o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        }
+                    } else {
+                        // 32 codes at a time, two lanes to a row
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int row = cw * 32 + i * 16 + (lane >> 1), c = lane & 1;
+                            const uint4 v = lds128(src + row * (C::KSUB * 32) + j * 32 + c * 16);
+                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t lo = w[e], hi = lo >> 4;
+                                sts128(dst + row * 128 + (((4 * c + e) ^ (row & 7)) << 4),
+                                       i4_pair(__byte_perm(lo, hi, 0x0400)),
+                                       i4_pair(__byte_perm(lo, hi, 0x0501)),
+                                       i4_pair(__byte_perm(lo, hi, 0x0602)),
+                                       i4_pair(__byte_perm(lo, hi, 0x0703)));
+                            }
+                        }
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(afull(ci & 1));
+                }
+                if (ok && lane == 0)
+                    mbar_arrive(empty(s));
+            }
+    }
+    __syncwarp();
+    if (SPLIT) {
+        cluster_sync();  // every rank's sums are in its shared memory
+        const int et = tid - 128;
+        if (et >= 0 && et < C::EW * 128 && !*fail) {
+            const int tile = first;
+            const int n0 = (tile / p.tiles_m) * rows_out, m0 = (tile % p.tiles_m) * NT;
+            const int rows = rows_out / split;  // this rank's rows of the tile
+            const int cols = min(NT, p.e.m - m0);
+            for (int i = et; i < rows * cols; i += C::EW * 128) {
+                const int r = rank * rows + i % rows, c = i / rows;
+                const uint32_t at = ring + (uint32_t)(c * 128 + r) * 4;
+                float a = 0.f, u = 0.f;
+                for (int k = 0; k < split; ++k) {  // in order: the same bits every time
+                    a += ld_cluster(at, k);
+                    if (gated)
+                        u += ld_cluster(at + 64 * 4, k);
+                }
+                if (n0 + r < p.e.n)
+                    emit(p.e, row_const(p.e, n0 + r), m0 + c, n0 + r, a, u);
+            }
+        }
+        cluster_sync();  // no CTA leaves while another reads its shared memory
+    } else {
+        __syncthreads();
+    }
+    if (tid == 0 && *fail)
+        atomicAdd(&g_timeouts, 1u);
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc<C::COLS>(tmem);
+    }
+}
+
+template <int QUANT, int NT, bool SPLIT, bool PROMOTE>
+cudaError_t launch_one(const TcParams &p, int grid, cudaStream_t stream)
+{
+    using C = Cfg<QUANT, NT, SPLIT, PROMOTE>;
+    auto kernel = linear_tc<QUANT, NT, SPLIT, PROMOTE>;
+    // the shared memory is allowed once per device (by whichever thread comes first)
+    static std::atomic<uint64_t> allowed{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev >= 64 || !(allowed.load(std::memory_order_relaxed) >> dev & 1)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (e != cudaSuccess)
+            return e;
+        if (dev < 64)
+            allowed.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    if (SPLIT) {
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = (unsigned)p.split;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+    }
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int QUANT>
+cudaError_t launch_variant(const Variant &v, const TcParams &p, int grid, cudaStream_t stream)
+{
+    if (v.split)
+        switch (v.nt) {
+        case 16: return launch_one<QUANT, 16, true, true>(p, grid, stream);
+        case 32: return launch_one<QUANT, 32, true, true>(p, grid, stream);
+        case 64: return launch_one<QUANT, 64, true, true>(p, grid, stream);
+        default: return launch_one<QUANT, 128, true, true>(p, grid, stream);
+        }
+    // eight draining warps hold 256 columns of 128 sums in registers; beside
+    // four converting warps there is room for half of them
+    constexpr int WIDE = QUANT == AMK_QUANT_BF16 ? 256 : 128;
+    if (v.promote || QUANT == AMK_QUANT_W4A16)
+        return launch_one<QUANT, WIDE, false, true>(p, grid, stream);
+    if constexpr (QUANT != AMK_QUANT_W4A16)
+        return launch_one<QUANT, 256, false, false>(p, grid, stream);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+}  // namespace linear
+}  // namespace amk
+
+#endif

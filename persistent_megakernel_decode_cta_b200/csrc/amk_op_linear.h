@@ -1,0 +1,53 @@
+// amk_op_linear.h -- what the kernels of amk_linear share.
+#ifndef AMK_OP_LINEAR_H
+#define AMK_OP_LINEAR_H
+
+#include <cuda.h>
+
+#include "amk_ops.h"
+
+namespace amk {
+namespace linear {
+
+// The epilogue of an output: act(a + bias) [* (u + up_bias)] [+ residual].
+struct Epilogue {
+    const uint16_t *bias, *up_bias;      // bf16 [n], or null
+    const uint16_t *w_scale, *up_scale;  // fp16 row scales (W8A16), or null
+    const void *residual;
+    void *y;
+    int64_t ldr, ldy;
+    int32_t m, n, act, gated, res_f32, y_f32;
+};
+
+// A launch of the tensor-core kernel.
+struct TcParams {
+    CUtensorMap x, w, up;
+    const uint16_t *w_gs, *up_gs;  // int4 group scales [n][groups]
+    int32_t groups;
+    int32_t blocks;                // K blocks
+    int32_t seg;                   // K blocks summed before their sum is added in fp32
+    int32_t tiles_m, tiles;
+    int32_t split;                 // CTAs of a cluster that share a tile's K
+    Epilogue e;
+};
+
+// One variant: `nt` tokens by 128 rows of weights to a tile.
+struct Variant {
+    int nt;
+    bool split;    // a cluster to a tile, its CTAs sharing K; else CTAs that walk the tiles
+    bool promote;  // sums of `seg` K blocks are added up in fp32 registers
+};
+
+// Launches the variant for a weight format (in its own source file each).
+cudaError_t launch_bf16(const Variant &v, const TcParams &p, int grid, cudaStream_t stream);
+cudaError_t launch_int8(const Variant &v, const TcParams &p, int grid, cudaStream_t stream);
+cudaError_t launch_int4(const Variant &v, const TcParams &p, int grid, cudaStream_t stream);
+// CTAs of these kernels that gave up a wait on the current device.
+cudaError_t timeouts_bf16(uint32_t *n);
+cudaError_t timeouts_int8(uint32_t *n);
+cudaError_t timeouts_int4(uint32_t *n);
+
+}  // namespace linear
+}  // namespace amk
+
+#endif
