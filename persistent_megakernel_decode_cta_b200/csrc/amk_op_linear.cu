@@ -280,7 +280,7 @@ Choice choose(const amk_linear_args *a, int sms)
         const int64_t tiles = tn * (((int64_t)a->m + nt - 1) / nt);
         if (nt > 16 && a->m <= nt / 2)
             continue;
-        const int per_sm = nt <= 64 ? 2 : 1;
+        const int per_sm = nt <= (codes ? 32 : 64) ? 2 : 1;
         for (int split = 1; split <= 8 && split <= (a->k + 127) / 128; split *= 2) {
             const int64_t waves = (tiles * split + (int64_t)sms * per_sm - 1) / (sms * per_sm);
             const double block = (2.0 * nt > 400 ? 2.0 * nt : 400) * per_sm;

@@ -74,6 +74,57 @@ __device__ __forceinline__ void store_at(const Epilogue &e, int64_t m, int n, fl
     else
         static_cast<uint16_t *>(e.y)[m * e.ldy + n] = f_bf16(v);
 }
+// 16 tokens of a row at once: nc of them are there.
+__device__ __forceinline__ void activate16(int act, float (&v)[16])
+{
+    if (act == AMK_ACT_SILU) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+            v[c] = activate(AMK_ACT_SILU, v[c]);
+    } else if (act == AMK_ACT_RELU) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+            v[c] = activate(AMK_ACT_RELU, v[c]);
+    } else {
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+            v[c] = activate(AMK_ACT_GELU, v[c]);
+    }
+}
+__device__ __forceinline__ void residual16(const Epilogue &e, int64_t m, int n, int nc,
+                                           float (&v)[16])
+{
+    const int64_t at = m * e.ldr + n;
+    if (e.res_f32) {
+        const float *r = static_cast<const float *>(e.residual) + at;
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+            v[c] = c < nc ? r[c * e.ldr] : 0.f;
+    } else {
+        const uint16_t *r = static_cast<const uint16_t *>(e.residual) + at;
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+            v[c] = c < nc ? bf16f(r[c * e.ldr]) : 0.f;
+    }
+}
+__device__ __forceinline__ void store16(const Epilogue &e, int64_t m, int n, int nc,
+                                        const float (&v)[16])
+{
+    const int64_t at = m * e.ldy + n;
+    if (e.y_f32) {
+        float *y = static_cast<float *>(e.y) + at;
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+            if (c < nc)
+                y[c * e.ldy] = v[c];
+    } else {
+        uint16_t *y = static_cast<uint16_t *>(e.y) + at;
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+            if (c < nc)
+                y[c * e.ldy] = f_bf16(v[c]);
+    }
+}
 // One output from its sums.
 __device__ __forceinline__ void emit(const Epilogue &e, const RowConst &c, int m, int n, float a,
                                      float u)
@@ -116,24 +167,41 @@ struct Cfg {
                                : QUANT == AMK_QUANT_W4A16 ? KSUB * 32 * 128
                                                           : 0;
     static constexpr int STAGE = X + (RAW ? RAW : A);
-    static constexpr int ASTAGES = RAW ? 2 : 0;  // converted blocks
+    static constexpr int ASTAGES = RAW ? 3 : 0;  // converted blocks
+    static constexpr int CW = RAW ? 8 : 0;       // converting warps
+    static constexpr int NB = NT <= 64 ? 4 : 2;  // accumulators
     static constexpr int XCH = SPLIT ? 0 : 2 * 2 * 16 * 64 * 4;
+    static constexpr int CTAS = SPLIT && NT <= (RAW ? 32 : 64) ? 2 : 1;  // to an SM
     // of an SM's 227 KB: half for a CTA where weights stream (two CTAs to an SM
     // keep the stream going while one starts or ends), else all of it
-    static constexpr int ROOM = (SPLIT && NT <= 64 ? 112 * 1024 : 224 * 1024) - 2048 - XCH;
+    static constexpr int ROOM = (CTAS == 2 ? 112 * 1024 : 224 * 1024) - 2048 - XCH;
     static constexpr int FIT = (ROOM - ASTAGES * BLK) / STAGE;
     static constexpr int STAGES = FIT > 8 ? 8 : FIT;
     static constexpr int SMEM = STAGES * STAGE + ASTAGES * BLK + XCH + 1024;
     static constexpr int EW = NT >= 64 ? 2 : 1;  // draining warpgroups
     static constexpr int NC = NT / EW;           // columns of each
-    static constexpr int THREADS = 128 + EW * 128 + (RAW ? 128 : 0);
-    static constexpr int CTAS = SPLIT && NT <= 64 ? 2 : 1;  // to an SM
-    static constexpr int COLS = 2 * NT < 32 ? 32 : 2 * NT;  // TMEM columns
+    static constexpr int THREADS = 128 + EW * 128 + CW * 32;
+    // 640 threads are launched with 96 registers each: 128 x 40 + 256 x 152 +
+    // 256 x 56 of them are no more than that
+    static constexpr int REGS = CW && EW == 2 && CTAS == 1 ? 96 : 0;
+    static_assert(!REGS || 128 * 40 + 256 * 152 + 256 * 56 <= THREADS * REGS, "register split");
+    static constexpr int COLS = NB * NT;  // TMEM columns
     static_assert(STAGES >= 2, "a ring needs two stages");
     static_assert(!SPLIT || NT * 512 <= STAGES * STAGE + ASTAGES * BLK, "the sums reuse the ring");
 };
 
 __device__ unsigned int g_timeouts;  // CTAs that gave up a wait
+
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 template <int QUANT, int NT, bool SPLIT, bool PROMOTE>
 __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
@@ -143,7 +211,7 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
     using C = Cfg<QUANT, NT, SPLIT, PROMOTE>;
     constexpr bool CODES = QUANT != AMK_QUANT_BF16;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * C::STAGES + 2 * 2 + 4];
+    __shared__ __align__(8) uint64_t bars[2 * C::STAGES + 2 * C::ASTAGES + 2 * C::NB];
     __shared__ uint32_t tmem_slot;
     __shared__ int fail_flag;
     volatile int *fail = &fail_flag;
@@ -154,21 +222,23 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
     auto full = [&](int s) { return bar0 + 8 * s; };
     auto empty = [&](int s) { return bar0 + 8 * (C::STAGES + s); };
     auto afull = [&](int s) { return bar0 + 8 * (2 * C::STAGES + s); };
-    auto aempty = [&](int s) { return bar0 + 8 * (2 * C::STAGES + 2 + s); };
-    auto accf = [&](int b) { return bar0 + 8 * (2 * C::STAGES + 4 + b); };
-    auto acce = [&](int b) { return bar0 + 8 * (2 * C::STAGES + 6 + b); };
+    auto aempty = [&](int s) { return bar0 + 8 * (2 * C::STAGES + C::ASTAGES + s); };
+    auto accf = [&](int b) { return bar0 + 8 * (2 * C::STAGES + 2 * C::ASTAGES + b); };
+    auto acce = [&](int b) { return bar0 + 8 * (2 * C::STAGES + 2 * C::ASTAGES + C::NB + b); };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         fail_flag = 0;
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(full(s), 1);
-            mbar_init(empty(s), CODES ? 5 : 1);  // the MMAs, and the four converting warps
+            mbar_init(empty(s), 1 + C::CW);  // the MMAs, and the converting warps
         }
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(afull(s), 4);
+        for (int s = 0; s < C::ASTAGES; ++s) {
+            mbar_init(afull(s), C::CW);
             mbar_init(aempty(s), 1);
-            mbar_init(accf(s), 1);
-            mbar_init(acce(s), 4 * C::EW);
+        }
+        for (int b = 0; b < C::NB; ++b) {
+            mbar_init(accf(b), 1);
+            mbar_init(acce(b), 4 * C::EW);
         }
         mbar_init_fence();
         prefetch_map(&p.x);
@@ -182,6 +252,8 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
+    pdl_wait();    // nothing above touches global memory
+    pdl_launch();  // the next kernel's CTAs may take the room that ending CTAs leave
     const bool gated = p.e.gated;
     const int rows_out = gated ? 64 : 128;
     const int split = SPLIT ? p.split : 1, rank = SPLIT ? (int)(blockIdx.x % split) : 0;
@@ -190,7 +262,12 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
     const int kb0 = (int)((int64_t)p.blocks * rank / split);
     const int kb1 = (int)((int64_t)p.blocks * (rank + 1) / split);
 
-    if (warp == 0) {
+    // the wide kernels for codes: the draining warps hold the sums, and take the
+    // registers that the others give up
+    if (warp < 4) {
+      if constexpr (C::REGS != 0)
+          setmaxnreg_dec<40>();
+      if (warp == 0) {
         if (lane == 0) {
             uint32_t it = 0;
             bool ok = true;
@@ -224,21 +301,22 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
             }
             if (!ok)  // no copy may land after the CTA has gone
                 for (uint32_t j = it > C::STAGES ? it - C::STAGES : 0; j < it; ++j) {
-                    const uint64_t t0 = gtimer();
+                    const long long t0 = clock64();
                     while (!mbar_try_wait(full(j % C::STAGES), (j / C::STAGES) & 1) &&
-                           gtimer() - t0 < 1000000000ull) {
+                           clock64() - t0 < 2000000000ll) {
                     }
                 }
         }
-    } else if (warp == 1) {
+      } else if (warp == 1) {
         if (lane == 0) {
             constexpr uint32_t idesc = tc_idesc(128, NT);
-            uint32_t it = 0, sc = 0;
+            uint32_t it = 0, sc = 0, aph = 0;
+            int as = 0;
             bool ok = true;
             for (int tile = first; tile < p.tiles && ok; tile += step) {
                 for (int kb = kb0; kb < kb1 && ok; ++sc) {
-                    const int b = sc & 1, end = min(kb + p.seg, kb1);
-                    if (!mbar_wait(acce(b), ((sc >> 1) & 1) ^ 1, fail)) {
+                    const int b = sc % C::NB, end = min(kb + p.seg, kb1);
+                    if (!mbar_wait(acce(b), ((sc / C::NB) & 1) ^ 1, fail)) {
                         ok = false;
                         break;
                     }
@@ -255,9 +333,8 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
                         for (int j = 0; j < C::KSUB; ++j) {
                             uint32_t ws = xs + C::X + j * C::BLK;
                             if (CODES) {
-                                const uint32_t ci = it * C::KSUB + j;
-                                ws = abuf + (ci & 1) * C::BLK;
-                                if (!mbar_wait(afull(ci & 1), (ci >> 1) & 1, fail)) {
+                                ws = abuf + as * C::BLK;
+                                if (!mbar_wait(afull(as), aph, fail)) {
                                     ok = false;
                                     break;
                                 }
@@ -270,8 +347,13 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
                                        accumulate);
                                 accumulate = 1;
                             }
-                            if (CODES)
-                                tc_commit(aempty((it * C::KSUB + j) & 1));
+                            if (CODES) {
+                                tc_commit(aempty(as));
+                                if (++as == C::ASTAGES) {
+                                    as = 0;
+                                    aph ^= 1;
+                                }
+                            }
                         }
                         tc_commit(empty(s));
                     }
@@ -280,7 +362,10 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
                 }
             }
         }
-    } else if (warp >= 4 && warp < 4 + 4 * C::EW) {
+      }
+    } else if (warp < 4 + 4 * C::EW) {
+        if constexpr (C::REGS != 0)
+            setmaxnreg_inc<152>();
         const int wg = (warp - 4) >> 2, q = warp & 3, r = q * 32 + lane;  // row of the tile
         const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + wg * C::NC;
         uint32_t sc = 0;
@@ -299,14 +384,14 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
                     acc[c] = 0.f;
                 uint16_t next = gs ? gs[kb0] : (uint16_t)0;  // seg = a group of 128 = a block
                 for (int kb = kb0; kb < kb1; kb += p.seg, ++sc) {
-                    const int b = sc & 1;
+                    const int b = sc % C::NB;
                     float scale = 1.f;
                     if (QUANT == AMK_QUANT_W4A16) {
                         scale = fp16f(next);
                         if (gs && kb + p.seg < kb1)
                             next = gs[kb + p.seg];
                     }
-                    if (!warp_wait(accf(b), (sc >> 1) & 1, fail)) {
+                    if (!warp_wait(accf(b), (sc / C::NB) & 1, fail)) {
                         ok = false;
                         break;
                     }
@@ -321,6 +406,20 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
                             acc[c0 + c] = QUANT == AMK_QUANT_W4A16
                                               ? fmaf(v[c], scale, acc[c0 + c])
                                               : acc[c0 + c] + v[c];
+                    }
+                    if (!SPLIT && kb + p.seg >= kb1) {
+                        // the tile's sums go back into the last buffer, from where
+                        // the loop below takes them a few columns at a time
+#pragma unroll
+                        for (int c0 = 0; c0 < C::NC; c0 += 16) {
+                            float v[16];
+#pragma unroll
+                            for (int c = 0; c < 16; ++c)
+                                v[c] = acc[c0 + c];
+                            tmem_st16(taddr + b * NT + c0, v);
+                        }
+                        tmem_st_wait();
+                        break;
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -337,9 +436,9 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
                 for (int c = 0; c < C::NC; ++c)
                     sts32f(ring + (uint32_t)((wg * C::NC + c) * 128 + r) * 4, acc[c]);
             } else {
-                const int b = sc & 1;
+                const int b = sc % C::NB;
                 if (!PROMOTE) {
-                    if (!warp_wait(accf(b), (sc >> 1) & 1, fail)) {
+                    if (!warp_wait(accf(b), (sc / C::NB) & 1, fail)) {
                         ok = false;
                         break;
                     }
@@ -347,92 +446,95 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
                 }
                 const RowConst rc = row_const(p.e, n);
                 const int cols = min(C::NC, p.e.m - m0 - wg * C::NC);  // tokens there are
-#pragma unroll
-                for (int c0 = 0; c0 < C::NC; c0 += 16) {
+                const bool mine = n < p.e.n && !is_up;
+                // rolled: unrolled, the loop would not fit the instruction cache
+#pragma unroll 1
+                for (int c0 = 0; c0 < cols; c0 += 16) {
                     float v[16];
-                    if constexpr (PROMOTE) {
-#pragma unroll
-                        for (int c = 0; c < 16; ++c)
-                            v[c] = acc[c0 + c];
-                    } else {
-                        tmem_ld16(taddr + b * NT + c0, v);
-                        tmem_ld_wait();
-                        if (c0 + 16 == C::NC) {  // the buffer has been read
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0)
-                                mbar_arrive(acce(b));
-                        }
-                    }
-                    if (c0 >= cols)
-                        continue;
+                    tmem_ld16(taddr + b * NT + c0, v);
                     const int64_t mc = (int64_t)m0 + wg * C::NC + c0;
-                    const bool mine = n < p.e.n && !is_up;
+                    const int nc = mine ? cols - c0 : 0;
                     float res[16];
-                    if (p.e.residual) {
+                    if (p.e.residual)
+                        residual16(p.e, mc, n, nc, res);
+                    tmem_ld_wait();
+                    if (!is_up) {
 #pragma unroll
                         for (int c = 0; c < 16; ++c)
-                            res[c] = mine && c0 + c < cols ? residual_at(p.e, mc + c, n) : 0.f;
+                            v[c] = fmaf(v[c], rc.ws, rc.bias);
+                        if (p.e.act != AMK_ACT_NONE)
+                            activate16(p.e.act, v);
                     }
                     // a gated row's other half sits 64 lanes on: through shared memory,
                     // in two buffers by turns so that one barrier a round suffices
-                    const uint32_t xb =
-                        xch + (uint32_t)((wg * 2 + ((c0 >> 4) & 1)) * 16 * 64) * 4;
                     if (gated) {
+                        const uint32_t xb =
+                            xch + (uint32_t)((wg * 2 + ((c0 >> 4) & 1)) * 16 * 64 + (r & 63)) * 4;
                         if (is_up) {
 #pragma unroll
                             for (int c = 0; c < 16; ++c)
-                                sts32f(xb + (uint32_t)(c * 64 + r - 64) * 4,
-                                       fmaf(v[c], rc.us, rc.ubias));
+                                sts32f(xb + c * 256, fmaf(v[c], rc.us, rc.ubias));
                         }
                         named_bar(1 + wg, 128);
-                    }
-                    if (mine) {
+                        if (!is_up) {
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            if (c0 + c < cols) {
-                                float o = activate(p.e.act, fmaf(v[c], rc.ws, rc.bias));
-                                if (gated)
-                                    o *= lds32f(xb + (uint32_t)(c * 64 + r) * 4);
-                                if (p.e.residual)
-                                    o += res[c];
-                                store_at(p.e, mc + c, n, o);
-                            }
+                            for (int c = 0; c < 16; ++c)
+                                v[c] *= lds32f(xb + c * 256);
                         }
                     }
+                    if (p.e.residual) {
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            v[c] += res[c];
+                    }
+                    store16(p.e, mc, n, nc, v);
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(acce(b));
                 if (gated)  // both buffers are read before the next tile writes them
                     named_bar(1 + wg, 128);
-                if (!PROMOTE)
-                    ++sc;
+                ++sc;
             }
         }
-    } else if (CODES && warp >= 4 + 4 * C::EW) {
-        const int cw = warp - 4 - 4 * C::EW;  // converting warp 0 .. 3
-        uint32_t it = 0;
+    } else if constexpr (CODES) {
+        if constexpr (C::REGS != 0)
+            setmaxnreg_dec<56>();
+        const int cw = warp - 4 - 4 * C::EW;  // converts rows 16 cw .. 16 cw + 15
+        uint32_t it = 0, aph = 1;
+        int as = 0;
         bool ok = true;
         for (int tile = first; tile < p.tiles && ok; tile += step)
-            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+            for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
                 const int s = it % C::STAGES;
                 if (!warp_wait(full(s), (it / C::STAGES) & 1, fail)) {
                     ok = false;
                     break;
                 }
                 const uint32_t src = ring + s * C::STAGE + C::X;
-                for (int j = 0; j < C::KSUB && ok; ++j) {
-                    const uint32_t ci = it * C::KSUB + j;
-                    if (!warp_wait(aempty(ci & 1), ((ci >> 1) & 1) ^ 1, fail)) {
+#pragma unroll
+                for (int j = 0; j < C::KSUB; ++j) {
+                    uint4 v[2];
+                    if (QUANT == AMK_QUANT_W8A16) {  // 16 codes at a time, four lanes to a row
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            v[i] = lds128(src + (cw * 16 + i * 8 + (lane >> 2)) * (C::KSUB * 64) +
+                                          j * 64 + (lane & 3) * 16);
+                    } else {  // 32 codes at a time, two lanes to a row
+                        v[0] = lds128(src + (cw * 16 + (lane >> 1)) * (C::KSUB * 32) + j * 32 +
+                                      (lane & 1) * 16);
+                    }
+                    if (!warp_wait(aempty(as), aph, fail)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t dst = abuf + (ci & 1) * C::BLK;
+                    const uint32_t dst = abuf + as * C::BLK;
                     if (QUANT == AMK_QUANT_W8A16) {
-                        // 16 codes at a time, four lanes to a row
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int row = cw * 32 + i * 8 + (lane >> 2), c = lane & 3;
-                            const uint4 v = lds128(src + row * (C::KSUB * 64) + j * 64 + c * 16);
-                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                        for (int i = 0; i < 2; ++i) {
+                            const int row = cw * 16 + i * 8 + (lane >> 2), c = lane & 3;
+                            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
                             uint32_t o[8];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
@@ -445,30 +547,30 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
                                        o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                         }
                     } else {
-                        // 32 codes at a time, two lanes to a row
+                        const int row = cw * 16 + (lane >> 1), c = lane & 1;
+                        const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int row = cw * 32 + i * 16 + (lane >> 1), c = lane & 1;
-                            const uint4 v = lds128(src + row * (C::KSUB * 32) + j * 32 + c * 16);
-                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint32_t lo = w[e], hi = lo >> 4;
-                                sts128(dst + row * 128 + (((4 * c + e) ^ (row & 7)) << 4),
-                                       i4_pair(__byte_perm(lo, hi, 0x0400)),
-                                       i4_pair(__byte_perm(lo, hi, 0x0501)),
-                                       i4_pair(__byte_perm(lo, hi, 0x0602)),
-                                       i4_pair(__byte_perm(lo, hi, 0x0703)));
-                            }
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t lo = w[e], hi = lo >> 4;
+                            sts128(dst + row * 128 + (((4 * c + e) ^ (row & 7)) << 4),
+                                   i4_pair(__byte_perm(lo, hi, 0x0400)),
+                                   i4_pair(__byte_perm(lo, hi, 0x0501)),
+                                   i4_pair(__byte_perm(lo, hi, 0x0602)),
+                                   i4_pair(__byte_perm(lo, hi, 0x0703)));
                         }
                     }
                     fence_async_smem();
                     __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(afull(ci & 1));
+                    if (lane == 0) {
+                        mbar_arrive(afull(as));
+                        if (j == C::KSUB - 1)
+                            mbar_arrive(empty(s));
+                    }
+                    if (++as == C::ASTAGES) {
+                        as = 0;
+                        aph ^= 1;
+                    }
                 }
-                if (ok && lane == 0)
-                    mbar_arrive(empty(s));
             }
     }
     __syncwarp();
@@ -480,17 +582,31 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
             const int n0 = (tile / p.tiles_m) * rows_out, m0 = (tile % p.tiles_m) * NT;
             const int rows = rows_out / split;  // this rank's rows of the tile
             const int cols = min(NT, p.e.m - m0);
-            for (int i = et; i < rows * cols; i += C::EW * 128) {
-                const int r = rank * rows + i % rows, c = i / rows;
-                const uint32_t at = ring + (uint32_t)(c * 128 + r) * 4;
+            const int r = rank * rows + et % rows, n = n0 + r, dc = C::EW * 128 / rows;
+            const RowConst rc = row_const(p.e, n);
+            uint32_t at[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                at[k] = map_rank(ring + (uint32_t)r * 4, k < split ? k : 0);
+            // added in the ranks' order: the same bits every time
+            for (int c = et / rows; c < cols && n < p.e.n; c += dc) {
+                float v[8], w[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < split) {
+                        v[k] = ld_cluster(at[k] + c * 512);
+                        if (gated)
+                            w[k] = ld_cluster(at[k] + c * 512 + 64 * 4);
+                    }
                 float a = 0.f, u = 0.f;
-                for (int k = 0; k < split; ++k) {  // in order: the same bits every time
-                    a += ld_cluster(at, k);
-                    if (gated)
-                        u += ld_cluster(at + 64 * 4, k);
-                }
-                if (n0 + r < p.e.n)
-                    emit(p.e, row_const(p.e, n0 + r), m0 + c, n0 + r, a, u);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < split) {
+                        a += v[k];
+                        if (gated)
+                            u += w[k];
+                    }
+                emit(p.e, rc, m0 + c, n, a, u);
             }
         }
         cluster_sync();  // no CTA leaves while another reads its shared memory
@@ -528,14 +644,14 @@ cudaError_t launch_one(const TcParams &p, int grid, cudaStream_t stream)
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = stream;
-    cudaLaunchAttribute attr{};
-    if (SPLIT) {
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = (unsigned)p.split;
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-    }
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = SPLIT ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 

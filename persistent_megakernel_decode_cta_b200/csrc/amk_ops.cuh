@@ -35,13 +35,6 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p)
 {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
-__device__ __forceinline__ uint64_t gtimer()
-{
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-
 // ---- mbarriers -----------------------------------------------------------------
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
 {
@@ -80,17 +73,16 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 {
     if (mbar_try_wait(bar, parity))
         return true;
-    const uint64_t t0 = gtimer();
+    const long long t0 = clock64();
     for (uint32_t i = 1; i < (1u << 28); ++i) {
         if (mbar_try_wait(bar, parity))
             return true;
-        if ((i & 63) == 0 && (*fail || gtimer() - t0 > 1000000000ull))
+        if ((i & 63) == 0 && (*fail || clock64() - t0 > 2000000000ll))
             break;
     }
     *fail = 1;
     return false;
 }
-
 // The same by a whole warp, whose lanes stay together and agree.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *fail)
 {
@@ -195,9 +187,37 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&v)[16])
           "=r"(r[14]), "=r"(r[15])
         : "r"(addr));
 }
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const float (&v)[16])
+{
+    const uint32_t *r = reinterpret_cast<const uint32_t *>(v);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,"
+        "%12,%13,%14,%15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+        "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+        "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait()
+{
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void tmem_ld_wait()
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// ---- launches that overlap -------------------------------------------------------
+// A kernel launched with programmatic stream serialization starts while the
+// one before it ends: its part before pdl_wait (which touches no global
+// memory) runs ahead, and pdl_wait returns once the earlier kernels of the
+// stream have finished and their writes are visible.
+__device__ __forceinline__ void pdl_wait()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_launch()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ---- clusters ------------------------------------------------------------------
@@ -208,16 +228,17 @@ __device__ __forceinline__ void cluster_sync()
     __syncthreads();
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
-__device__ __forceinline__ float ld_cluster(uint32_t smem, uint32_t rank)
+// the address of a shared-memory location in the cluster's CTA `rank`
+__device__ __forceinline__ uint32_t map_rank(uint32_t smem, uint32_t rank)
+{
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr)
 {
     float v;
-    asm volatile(
-        "{\n\t.reg .b32 a;\n\t"
-        "mapa.shared::cluster.u32 a, %1, %2;\n\t"
-        "ld.shared::cluster.f32 %0, [a];\n\t}"
-        : "=f"(v)
-        : "r"(smem), "r"(rank)
-        : "memory");
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
 }
 
