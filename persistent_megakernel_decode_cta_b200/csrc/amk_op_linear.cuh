@@ -265,66 +265,69 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
     // the wide kernels for codes: the draining warps hold the sums, and take the
     // registers that the others give up
     if (warp < 4) {
-      if constexpr (C::REGS != 0)
-          setmaxnreg_dec<40>();
-      if (warp == 0) {
-        if (lane == 0) {
-            uint32_t it = 0;
+        if constexpr (C::REGS != 0)
+            setmaxnreg_dec<40>();
+        if (warp == 0) {
+            uint32_t it = 0, ph = 1;
+            int s = 0;
             bool ok = true;
             for (int tile = first; tile < p.tiles && ok; tile += step) {
                 const int n0 = (tile / p.tiles_m) * rows_out, m0 = (tile % p.tiles_m) * NT;
                 for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const int s = it % C::STAGES;
-                    if (!mbar_wait(empty(s), ((it / C::STAGES) & 1) ^ 1, fail)) {
+                    if (!warp_wait(empty(s), ph, fail)) {
                         ok = false;
                         break;
                     }
                     const uint32_t xs = ring + s * C::STAGE, ws = xs + C::X;
                     const int k = kb * C::KSUB * 64;
-                    mbar_expect_tx(full(s), C::STAGE);
-                    if (CODES) {
-                        const int kx = QUANT == AMK_QUANT_W8A16 ? k : k / 2;
-                        tma_2d(ws, &p.w, kx, n0, full(s));
-                        if (gated)
-                            tma_2d(ws + C::RAW / 2, &p.up, kx, n0, full(s));
-                    }
-#pragma unroll
-                    for (int j = 0; j < C::KSUB; ++j) {
-                        if (!CODES) {
-                            tma_2d(ws + j * 16384, &p.w, k + j * 64, n0, full(s));
+                    if (elect_one()) {
+                        mbar_expect_tx(full(s), C::STAGE);
+                        if (CODES) {
+                            const int kx = QUANT == AMK_QUANT_W8A16 ? k : k / 2;
+                            tma_2d(ws, &p.w, kx, n0, full(s));
                             if (gated)
-                                tma_2d(ws + j * 16384 + 8192, &p.up, k + j * 64, n0, full(s));
+                                tma_2d(ws + C::RAW / 2, &p.up, kx, n0, full(s));
                         }
-                        tma_2d(xs + j * NT * 128, &p.x, k + j * 64, m0, full(s));
+#pragma unroll
+                        for (int j = 0; j < C::KSUB; ++j) {
+                            if (!CODES) {
+                                tma_2d(ws + j * C::BLK, &p.w, k + j * 64, n0, full(s));
+                                if (gated)
+                                    tma_2d(ws + j * C::BLK + C::BLK / 2, &p.up, k + j * 64, n0,
+                                           full(s));
+                            }
+                            tma_2d(xs + j * NT * 128, &p.x, k + j * 64, m0, full(s));
+                        }
+                    }
+                    __syncwarp();
+                    if (++s == C::STAGES) {
+                        s = 0;
+                        ph ^= 1;
                     }
                 }
             }
-            if (!ok)  // no copy may land after the CTA has gone
+            if (!ok && lane == 0)  // no copy may land after the CTA has gone
                 for (uint32_t j = it > C::STAGES ? it - C::STAGES : 0; j < it; ++j) {
                     const long long t0 = clock64();
                     while (!mbar_try_wait(full(j % C::STAGES), (j / C::STAGES) & 1) &&
                            clock64() - t0 < 2000000000ll) {
                     }
                 }
-        }
-      } else if (warp == 1) {
-        if (lane == 0) {
+        } else if (warp == 1) {
             constexpr uint32_t idesc = tc_idesc(128, NT);
-            uint32_t it = 0, sc = 0, aph = 0;
-            int as = 0;
+            uint32_t sc = 0, ph = 0, aph = 0;
+            int s = 0, as = 0;
             bool ok = true;
             for (int tile = first; tile < p.tiles && ok; tile += step) {
                 for (int kb = kb0; kb < kb1 && ok; ++sc) {
                     const int b = sc % C::NB, end = min(kb + p.seg, kb1);
-                    if (!mbar_wait(acce(b), ((sc / C::NB) & 1) ^ 1, fail)) {
+                    if (!warp_wait(acce(b), ((sc / C::NB) & 1) ^ 1, fail)) {
                         ok = false;
                         break;
                     }
-                    tc_fence_after();
                     uint32_t accumulate = 0;
-                    for (; kb < end && ok; ++kb, ++it) {
-                        const int s = it % C::STAGES;
-                        if (!mbar_wait(full(s), (it / C::STAGES) & 1, fail)) {
+                    for (; kb < end && ok; ++kb) {
+                        if (!warp_wait(full(s), ph, fail)) {
                             ok = false;
                             break;
                         }
@@ -334,35 +337,41 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
                             uint32_t ws = xs + C::X + j * C::BLK;
                             if (CODES) {
                                 ws = abuf + as * C::BLK;
-                                if (!mbar_wait(afull(as), aph, fail)) {
+                                if (!warp_wait(afull(as), aph, fail)) {
                                     ok = false;
                                     break;
                                 }
                             }
                             tc_fence_after();
                             const uint64_t ad = tc_desc(ws), bd = tc_desc(xs + j * NT * 128);
+                            if (elect_one()) {
 #pragma unroll
-                            for (int k16 = 0; k16 < 4; ++k16) {  // 32 bytes of a row each
-                                tc_mma(tmem + b * NT, ad + 2 * k16, bd + 2 * k16, idesc,
-                                       accumulate);
-                                accumulate = 1;
-                            }
-                            if (CODES) {
-                                tc_commit(aempty(as));
-                                if (++as == C::ASTAGES) {
-                                    as = 0;
-                                    aph ^= 1;
+                                for (int k16 = 0; k16 < 4; ++k16)  // 32 bytes of a row each
+                                    tc_mma(tmem + b * NT, ad + 2 * k16, bd + 2 * k16, idesc,
+                                           k16 ? 1u : accumulate);
+                                if (CODES)
+                                    tc_commit(aempty(as));
+                                if (j == C::KSUB - 1) {
+                                    tc_commit(empty(s));
+                                    if (kb + 1 == end)
+                                        tc_commit(accf(b));
                                 }
                             }
+                            __syncwarp();
+                            accumulate = 1;
+                            if (CODES && ++as == C::ASTAGES) {
+                                as = 0;
+                                aph ^= 1;
+                            }
                         }
-                        tc_commit(empty(s));
+                        if (++s == C::STAGES) {
+                            s = 0;
+                            ph ^= 1;
+                        }
                     }
-                    if (ok)
-                        tc_commit(accf(b));
                 }
             }
         }
-      }
     } else if (warp < 4 + 4 * C::EW) {
         if constexpr (C::REGS != 0)
             setmaxnreg_inc<152>();
@@ -502,13 +511,12 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
         if constexpr (C::REGS != 0)
             setmaxnreg_dec<56>();
         const int cw = warp - 4 - 4 * C::EW;  // converts rows 16 cw .. 16 cw + 15
-        uint32_t it = 0, aph = 1;
-        int as = 0;
+        uint32_t ph = 0, aph = 1;
+        int s = 0, as = 0;
         bool ok = true;
         for (int tile = first; tile < p.tiles && ok; tile += step)
-            for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
-                const int s = it % C::STAGES;
-                if (!warp_wait(full(s), (it / C::STAGES) & 1, fail)) {
+            for (int kb = kb0; kb < kb1 && ok; ++kb) {
+                if (!warp_wait(full(s), ph, fail)) {
                     ok = false;
                     break;
                 }
@@ -570,6 +578,10 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
                         as = 0;
                         aph ^= 1;
                     }
+                }
+                if (++s == C::STAGES) {
+                    s = 0;
+                    ph ^= 1;
                 }
             }
     }
