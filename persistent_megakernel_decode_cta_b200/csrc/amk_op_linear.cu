@@ -309,6 +309,39 @@ Choice choose(const amk_linear_args *a, int sms)
     return best;
 }
 
+int launch_few(const amk_linear_args *a, const Epilogue &e, cudaStream_t stream)
+{
+    SkinnyParams p{};
+    p.x = static_cast<const uint16_t *>(a->x);
+    p.w = a->w;
+    p.up = a->up;
+    p.w_gs = static_cast<const uint16_t *>(a->w_scale);
+    p.up_gs = static_cast<const uint16_t *>(a->up_scale);
+    p.ldx = a->ldx;
+    p.k = a->k;
+    p.groups = (a->k + kQ4Group - 1) / kQ4Group;
+    p.row_bytes = a->quant == AMK_QUANT_BF16    ? 2 * (int64_t)a->k
+                  : a->quant == AMK_QUANT_W8A16 ? a->k
+                                                : a->k / 2;
+    p.e = e;
+    const int rows = a->up ? kSkinnyRows / 2 : kSkinnyRows;
+    const int64_t tiles = ((int64_t)a->n + rows - 1) / rows;
+    // more CTAs to a tile as long as they all run at once and a warp keeps some
+    // steps (64 bytes of a row); fewer steps only where the CTAs are few
+    p.split = 1;
+    while (p.split < 8 && tiles * p.split * 2 <= 2 * sm_count() &&
+           p.row_bytes / 64 >= kSkinnyKG * 2 * p.split * (tiles * p.split < 64 ? 3 : 8))
+        p.split *= 2;
+    cudaError_t err;
+    if (a->quant == AMK_QUANT_W8A16)
+        err = skinny_int8(p, stream);
+    else if (a->quant == AMK_QUANT_W4A16)
+        err = skinny_int4(p, stream);
+    else
+        err = skinny_bf16(p, stream);
+    return launch_status(err, "amk_linear");
+}
+
 int launch_tc(const amk_linear_args *a, const Epilogue &e, cudaStream_t stream)
 {
     const int sms = sm_count();
@@ -400,7 +433,7 @@ extern "C" int amk_linear(const amk_linear_args *a, void *cuda_stream)
     p.e.y_f32 = a->y_type == AMK_DT_F32;
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     if (fits_tensor_cores(a))
-        return launch_tc(a, p.e, st);
+        return a->m <= kSkinnyTokens ? launch_few(a, p.e, st) : launch_tc(a, p.e, st);
     cudaError_t e;
     if (a->quant == AMK_QUANT_W8A16)
         e = launch_generic<AMK_QUANT_W8A16>(p, st);

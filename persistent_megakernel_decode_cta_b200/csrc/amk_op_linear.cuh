@@ -167,27 +167,27 @@ struct Cfg {
                                : QUANT == AMK_QUANT_W4A16 ? KSUB * 32 * 128
                                                           : 0;
     static constexpr int STAGE = X + (RAW ? RAW : A);
-    static constexpr int ASTAGES = RAW ? 3 : 0;  // converted blocks
+    static constexpr int ASTAGES = !RAW ? 0 : KSUB == 2 ? 2 : 3;  // converted stages
     static constexpr int CW = RAW ? 8 : 0;       // converting warps
     static constexpr int NB = NT <= 64 ? 4 : 2;  // accumulators
     static constexpr int XCH = SPLIT ? 0 : 2 * 2 * 16 * 64 * 4;
-    static constexpr int CTAS = SPLIT && NT <= (RAW ? 32 : 64) ? 2 : 1;  // to an SM
+    static constexpr int CTAS = SPLIT && NT <= (RAW ? 16 : 64) ? 2 : 1;  // to an SM
     // of an SM's 227 KB: half for a CTA where weights stream (two CTAs to an SM
     // keep the stream going while one starts or ends), else all of it
     static constexpr int ROOM = (CTAS == 2 ? 112 * 1024 : 224 * 1024) - 2048 - XCH;
-    static constexpr int FIT = (ROOM - ASTAGES * BLK) / STAGE;
+    static constexpr int FIT = (ROOM - ASTAGES * A) / STAGE;
     static constexpr int STAGES = FIT > 8 ? 8 : FIT;
-    static constexpr int SMEM = STAGES * STAGE + ASTAGES * BLK + XCH + 1024;
+    static constexpr int SMEM = STAGES * STAGE + ASTAGES * A + XCH + 1024;
     static constexpr int EW = NT >= 64 ? 2 : 1;  // draining warpgroups
     static constexpr int NC = NT / EW;           // columns of each
     static constexpr int THREADS = 128 + EW * 128 + CW * 32;
     // 640 threads are launched with 96 registers each: 128 x 40 + 256 x 152 +
     // 256 x 56 of them are no more than that
-    static constexpr int REGS = CW && EW == 2 && CTAS == 1 ? 96 : 0;
+    static constexpr int REGS = CW && EW == 2 ? 96 : 0;
     static_assert(!REGS || 128 * 40 + 256 * 152 + 256 * 56 <= THREADS * REGS, "register split");
     static constexpr int COLS = NB * NT;  // TMEM columns
     static_assert(STAGES >= 2, "a ring needs two stages");
-    static_assert(!SPLIT || NT * 512 <= STAGES * STAGE + ASTAGES * BLK, "the sums reuse the ring");
+    static_assert(!SPLIT || NT * 512 <= STAGES * STAGE + ASTAGES * A, "the sums reuse the ring");
 };
 
 __device__ unsigned int g_timeouts;  // CTAs that gave up a wait
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
     volatile int *fail = &fail_flag;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t abuf = ring + C::STAGES * C::STAGE;  // converted blocks
-    const uint32_t xch = abuf + C::ASTAGES * C::BLK;
+    const uint32_t xch = abuf + C::ASTAGES * C::A;
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8 * s; };
     auto empty = [&](int s) { return bar0 + 8 * (C::STAGES + s); };
@@ -326,43 +326,36 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
                         break;
                     }
                     uint32_t accumulate = 0;
-                    for (; kb < end && ok; ++kb) {
-                        if (!warp_wait(full(s), ph, fail)) {
+                    for (; kb < end; ++kb) {
+                        // converted weights come after their stage, and so after its x
+                        if (!(CODES ? warp_wait(afull(as), aph, fail)
+                                    : warp_wait(full(s), ph, fail))) {
                             ok = false;
                             break;
                         }
+                        tc_fence_after();
                         const uint32_t xs = ring + s * C::STAGE;
+                        const uint64_t ad = tc_desc(CODES ? abuf + as * C::A : xs + C::X);
+                        const uint64_t bd = tc_desc(xs);
+                        if (elect_one()) {
 #pragma unroll
-                        for (int j = 0; j < C::KSUB; ++j) {
-                            uint32_t ws = xs + C::X + j * C::BLK;
-                            if (CODES) {
-                                ws = abuf + as * C::BLK;
-                                if (!warp_wait(afull(as), aph, fail)) {
-                                    ok = false;
-                                    break;
-                                }
-                            }
-                            tc_fence_after();
-                            const uint64_t ad = tc_desc(ws), bd = tc_desc(xs + j * NT * 128);
-                            if (elect_one()) {
+                            for (int j = 0; j < C::KSUB; ++j)
 #pragma unroll
                                 for (int k16 = 0; k16 < 4; ++k16)  // 32 bytes of a row each
-                                    tc_mma(tmem + b * NT, ad + 2 * k16, bd + 2 * k16, idesc,
-                                           k16 ? 1u : accumulate);
-                                if (CODES)
-                                    tc_commit(aempty(as));
-                                if (j == C::KSUB - 1) {
-                                    tc_commit(empty(s));
-                                    if (kb + 1 == end)
-                                        tc_commit(accf(b));
-                                }
-                            }
-                            __syncwarp();
-                            accumulate = 1;
-                            if (CODES && ++as == C::ASTAGES) {
-                                as = 0;
-                                aph ^= 1;
-                            }
+                                    tc_mma(tmem + b * NT, ad + j * (C::BLK >> 4) + 2 * k16,
+                                           bd + j * (NT * 128 >> 4) + 2 * k16, idesc,
+                                           j + k16 ? 1u : accumulate);
+                            if (CODES)
+                                tc_commit(aempty(as));
+                            tc_commit(empty(s));
+                            if (kb + 1 == end)
+                                tc_commit(accf(b));
+                        }
+                        __syncwarp();
+                        accumulate = 1;
+                        if (CODES && ++as == C::ASTAGES) {
+                            as = 0;
+                            aph ^= 1;
                         }
                         if (++s == C::STAGES) {
                             s = 0;
@@ -521,63 +514,58 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
                     break;
                 }
                 const uint32_t src = ring + s * C::STAGE + C::X;
+                constexpr int NV = C::RAW / (C::CW * 512);  // 16-byte pieces of a lane
+                uint4 v[NV];
 #pragma unroll
-                for (int j = 0; j < C::KSUB; ++j) {
-                    uint4 v[2];
-                    if (QUANT == AMK_QUANT_W8A16) {  // 16 codes at a time, four lanes to a row
+                for (int i = 0; i < NV; ++i)  // the warp's 16 rows of codes, in order
+                    v[i] = lds128(src + cw * (C::RAW / C::CW) + i * 512 + lane * 16);
+                if (!warp_wait(aempty(as), aph, fail)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t dst = abuf + as * C::A;
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            v[i] = lds128(src + (cw * 16 + i * 8 + (lane >> 2)) * (C::KSUB * 64) +
-                                          j * 64 + (lane & 3) * 16);
-                    } else {  // 32 codes at a time, two lanes to a row
-                        v[0] = lds128(src + (cw * 16 + (lane >> 1)) * (C::KSUB * 32) + j * 32 +
-                                      (lane & 1) * 16);
-                    }
-                    if (!warp_wait(aempty(as), aph, fail)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t dst = abuf + as * C::BLK;
+                for (int i = 0; i < NV; ++i) {
+                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
                     if (QUANT == AMK_QUANT_W8A16) {
+                        // a piece is 16 codes; KSUB * 4 of them make a row
+                        const int at = i * 32 + lane;
+                        const int row = cw * 16 + at / (C::KSUB * 4), pc = at % (C::KSUB * 4);
+                        const uint32_t d = dst + (pc >> 2) * C::BLK + row * 128;
+                        const int c = 2 * (pc & 3);
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int row = cw * 16 + i * 8 + (lane >> 2), c = lane & 3;
-                            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                            uint32_t o[8];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                o[2 * e] = i8_pair(__byte_perm(w[e], 0, 0x4140));
-                                o[2 * e + 1] = i8_pair(__byte_perm(w[e], 0, 0x4342));
-                            }
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                sts128(dst + row * 128 + (((2 * c + e) ^ (row & 7)) << 4),
-                                       o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                        }
+                        for (int e = 0; e < 2; ++e)
+                            sts128(d + (((c + e) ^ (row & 7)) << 4),
+                                   i8_pair(__byte_perm(w[2 * e], 0, 0x4140)),
+                                   i8_pair(__byte_perm(w[2 * e], 0, 0x4342)),
+                                   i8_pair(__byte_perm(w[2 * e + 1], 0, 0x4140)),
+                                   i8_pair(__byte_perm(w[2 * e + 1], 0, 0x4342)));
                     } else {
-                        const int row = cw * 16 + (lane >> 1), c = lane & 1;
-                        const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+                        // a piece is 32 codes; KSUB * 2 of them make a row
+                        const int at = i * 32 + lane;
+                        const int row = cw * 16 + at / (C::KSUB * 2), pc = at % (C::KSUB * 2);
+                        const uint32_t d = dst + (pc >> 1) * C::BLK + row * 128;
+                        const int c = 4 * (pc & 1);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const uint32_t lo = w[e], hi = lo >> 4;
-                            sts128(dst + row * 128 + (((4 * c + e) ^ (row & 7)) << 4),
+                            sts128(d + (((c + e) ^ (row & 7)) << 4),
                                    i4_pair(__byte_perm(lo, hi, 0x0400)),
                                    i4_pair(__byte_perm(lo, hi, 0x0501)),
                                    i4_pair(__byte_perm(lo, hi, 0x0602)),
                                    i4_pair(__byte_perm(lo, hi, 0x0703)));
                         }
                     }
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(afull(as));
-                        if (j == C::KSUB - 1)
-                            mbar_arrive(empty(s));
-                    }
-                    if (++as == C::ASTAGES) {
-                        as = 0;
-                        aph ^= 1;
-                    }
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(afull(as));
+                    mbar_arrive(empty(s));
+                }
+                if (++as == C::ASTAGES) {
+                    as = 0;
+                    aph ^= 1;
                 }
                 if (++s == C::STAGES) {
                     s = 0;

@@ -38,6 +38,23 @@ struct Variant {
     bool promote;  // sums of `seg` K blocks are added up in fp32 registers
 };
 
+// A launch of the kernel for few tokens.
+constexpr int kSkinnyTokens = 16;
+constexpr int kSkinnyRows = 64;  // rows of weights of a CTA: two groups of 32
+constexpr int kSkinnyKG = 4;     // warps that share a group's K
+struct SkinnyParams {
+    const uint16_t *x;
+    const void *w, *up;
+    const uint16_t *w_gs, *up_gs;  // int4 group scales [n][groups]
+    int64_t ldx, row_bytes;
+    int32_t k, groups;
+    int32_t split;                 // CTAs of a cluster that share K
+    Epilogue e;
+};
+cudaError_t skinny_bf16(const SkinnyParams &p, cudaStream_t stream);
+cudaError_t skinny_int8(const SkinnyParams &p, cudaStream_t stream);
+cudaError_t skinny_int4(const SkinnyParams &p, cudaStream_t stream);
+
 // Launches the variant for a weight format (in its own source file each).
 cudaError_t launch_bf16(const Variant &v, const TcParams &p, int grid, cudaStream_t stream);
 cudaError_t launch_int8(const Variant &v, const TcParams &p, int grid, cudaStream_t stream);

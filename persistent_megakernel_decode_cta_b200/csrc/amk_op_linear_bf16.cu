@@ -1,7 +1,7 @@
-// amk_op_linear_bf16.cu -- amk_linear's tensor-core kernels for bf16 weights.
+// amk_op_linear_bf16.cu -- amk_linear's kernels for bf16 weights.
 #include <atomic>
 
-#include "amk_op_linear.cuh"
+#include "amk_op_linear_skinny.cuh"
 
 namespace amk {
 namespace linear {
@@ -9,6 +9,11 @@ namespace linear {
 cudaError_t launch_bf16(const Variant &v, const TcParams &p, int grid, cudaStream_t stream)
 {
     return launch_variant<AMK_QUANT_BF16>(v, p, grid, stream);
+}
+
+cudaError_t skinny_bf16(const SkinnyParams &p, cudaStream_t stream)
+{
+    return launch_skinny_of<AMK_QUANT_BF16>(p, stream);
 }
 
 cudaError_t timeouts_bf16(uint32_t *n)

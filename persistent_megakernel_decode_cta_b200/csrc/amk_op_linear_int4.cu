@@ -1,7 +1,7 @@
-// amk_op_linear_int4.cu -- amk_linear's tensor-core kernels for int4 weights.
+// amk_op_linear_int4.cu -- amk_linear's kernels for int4 weights.
 #include <atomic>
 
-#include "amk_op_linear.cuh"
+#include "amk_op_linear_skinny.cuh"
 
 namespace amk {
 namespace linear {
@@ -9,6 +9,11 @@ namespace linear {
 cudaError_t launch_int4(const Variant &v, const TcParams &p, int grid, cudaStream_t stream)
 {
     return launch_variant<AMK_QUANT_W4A16>(v, p, grid, stream);
+}
+
+cudaError_t skinny_int4(const SkinnyParams &p, cudaStream_t stream)
+{
+    return launch_skinny_of<AMK_QUANT_W4A16>(p, stream);
 }
 
 cudaError_t timeouts_int4(uint32_t *n)

@@ -68,34 +68,37 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+constexpr uint32_t kSuspend = 20000;  // ns that a try may wait
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(bar), "r"(parity)
+        : "r"(bar), "r"(parity), "r"(kSuspend)
         : "memory");
     return ok != 0;
 }
-// Waits for the phase, for at most about a second (nothing waited for takes a
-// thousandth of that): false, and *fail set, when it gave up or another thread
-// of the CTA has.
+// Waits for the phase, each try suspended for up to kSuspend ns: false, and
+// *fail set, when it gave up after a second or more (nothing waited for takes
+// a thousandth of that).  Few instructions, and few tries: warps that poll
+// take the issue slots and the shared-memory pipe of those that work.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *fail)
 {
-    if (mbar_try_wait(bar, parity))
-        return true;
-    const long long t0 = clock64();
-    for (uint32_t i = 1; i < (1u << 28); ++i) {
-        if (mbar_try_wait(bar, parity))
-            return true;
-        if ((i & 63) == 0 && (*fail || clock64() - t0 > 2000000000ll))
-            break;
-    }
-    *fail = 1;
-    return false;
+    long long t0 = 0;
+#pragma unroll 1
+    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i)
+        if ((i & 1023) == 0) {
+            if (t0 == 0)
+                t0 = clock64();
+            else if (clock64() - t0 > 2000000000ll) {
+                *fail = 1;
+                return false;
+            }
+        }
+    return true;
 }
 // The same by a whole warp, whose lanes stay together and agree.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *fail)
