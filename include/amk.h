@@ -455,6 +455,12 @@ AMK_API int amk_decode_step_noalloc(const amk_plan *plan, const amk_weights *w, 
  * enqueued.  AMK_ERR_INVALID_ARG on a bad argument, AMK_ERR_NO_DEVICE without
  * a device, AMK_ERR_CUDA if a launch fails. */
 
+/* Every wait of these kernels is for copies and products of their own CTA and
+ * is bounded; a CTA that gives one up (after a second: a faulty device) leaves
+ * its outputs unwritten and is counted.  *n (host) = such CTAs on the current
+ * device since the library was loaded.  Synchronises the device. */
+AMK_API int amk_ops_timeouts(uint32_t *n);
+
 /* y = act(x w^T + bias) [* (x up^T + up_bias)] [+ residual]: a matrix product
  * with its epilogue; with `up` the gated pair of projections of an FFN.
  * x is bf16 [m][k], w and up are in one of the model's weight formats with

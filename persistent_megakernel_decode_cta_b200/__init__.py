@@ -14,7 +14,7 @@ from . import abi
 
 __all__ = ["AmkError", "Decoder", "Plan", "validate_graph", "default_options", "version",
            "make_config", "weights_struct", "decode_step_noalloc", "read_ceiling",
-           "linear", "attention", "verify_draft"]
+           "linear", "attention", "verify_draft", "ops_timeouts"]
 
 
 class AmkError(RuntimeError):
@@ -381,4 +381,4 @@ class Decoder:
             pass
 
 
-from .ops import attention, linear, verify_draft  # noqa: E402  (they use AmkError and _check)
+from .ops import attention, linear, ops_timeouts, verify_draft  # noqa: E402  (they use AmkError and _check)

@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct as struct_module
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libamk.so")
@@ -129,6 +130,18 @@ class VerifyArgs(ctypes.Structure):
         ("workspace_bytes", c_i64)]
 
 
+def packer(struct):
+    """A function that packs a structure's fields, in order (pointers as
+    integers), into bytes of its layout: a third of the time of filling the
+    ctypes object, which the operators' calls would otherwise spend most on."""
+    codes = {c_vp: "P", c_i32: "i", c_i64: "q", c_f32: "f"}
+    fmt = struct_module.Struct("@" + "".join(codes[t] for _, t in struct._fields_))
+    pad = ctypes.sizeof(struct) - fmt.size
+    if pad:
+        fmt = struct_module.Struct(fmt.format + f"{pad}x")
+    return fmt.pack
+
+
 # every function include/amk.h declares: name -> (restype, argtypes)
 SIGNATURES = {
     "amk_version": (ctypes.c_char_p, []),
@@ -161,10 +174,11 @@ SIGNATURES = {
                                         ctypes.POINTER(ctypes.c_double)]),
     "amk_decode_step_noalloc": (ctypes.c_int, [c_vp, ctypes.POINTER(Weights), c_vp, c_i32,
                                                c_i32, c_vp, ctypes.POINTER(c_i32), c_vp]),
-    "amk_linear": (ctypes.c_int, [ctypes.POINTER(LinearArgs), c_vp]),
-    "amk_attention": (ctypes.c_int, [ctypes.POINTER(AttentionArgs), c_vp]),
+    "amk_ops_timeouts": (ctypes.c_int, [ctypes.POINTER(c_u32)]),
+    "amk_linear": (ctypes.c_int, [c_vp, c_vp]),
+    "amk_attention": (ctypes.c_int, [c_vp, c_vp]),
     "amk_verify_workspace": (c_i64, [c_i32, c_i32]),
-    "amk_verify_draft": (ctypes.c_int, [ctypes.POINTER(VerifyArgs), c_vp]),
+    "amk_verify_draft": (ctypes.c_int, [c_vp, c_vp]),
 }
 
 _LIB = None

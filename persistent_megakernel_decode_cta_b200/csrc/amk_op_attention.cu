@@ -1,11 +1,15 @@
 // amk_op_attention.cu -- amk_attention: causal attention with a sliding window
 // and sinks over KV-cache rows.
+#include <atomic>
 #include <math.h>
 
+#include "amk_ops.cuh"
 #include "amk_ops.h"
 
 namespace amk {
 namespace {
+
+using namespace ops;
 
 struct AttnParams {
     const uint16_t *q, *k, *v;
@@ -14,20 +18,6 @@ struct AttnParams {
     int32_t T, pos, n_heads, group, hd, window, sinks;
     float scale_log2;  // scale * log2(e): weights are 2^(s - m)
 };
-
-__device__ __forceinline__ float bf16f(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
-__device__ __forceinline__ uint16_t f_bf16(float f)
-{
-    uint16_t r;
-    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(f));
-    return r;
-}
-__device__ __forceinline__ float exp2_fast(float x)
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 
 // The visible rows of position p: [0, s) and [lo, p].
 __device__ __forceinline__ void visible(const AttnParams &a, int p, int &s, int &lo)
@@ -41,9 +31,11 @@ __device__ __forceinline__ void visible(const AttnParams &a, int p, int &s, int 
 // then the lanes hold the output's elements and take the rows one after the
 // other.  Rows outside the mask are not touched, so nothing they hold can
 // reach the result.  qs: the warp's query in shared memory, pre-scaled, [hd].
+// Writes the elements d for which mine(d).
 constexpr int kMaxHd = 256;
 
-__device__ void attend_row(const AttnParams &a, int t, int h, const float *qs)
+template <typename Mine>
+__device__ void attend_row(const AttnParams &a, int t, int h, const float *qs, Mine mine)
 {
     const int lane = threadIdx.x & 31;
     const int p = a.pos + t, hd = a.hd;
@@ -69,8 +61,8 @@ __device__ void attend_row(const AttnParams &a, int t, int h, const float *qs)
         const float mn = nan ? NAN : fmaxf(m, mx);
         // -inf scores alone so far: weights of 0 and nothing to rescale
         const float base = mn == -INFINITY ? 0.f : mn;
-        const float pr = i < n ? exp2_fast(sc - base) : 0.f;
-        const float corr = exp2_fast(m - base);
+        const float pr = i < n ? ex2(sc - base) : 0.f;
+        const float corr = ex2(m - base);
         float sum = pr;
         for (int off = 16; off; off >>= 1)
             sum += __shfl_xor_sync(0xffffffffu, sum, off);
@@ -93,12 +85,14 @@ __device__ void attend_row(const AttnParams &a, int t, int h, const float *qs)
     uint16_t *out = a.out + t * a.o_ts + h * a.o_hs;
 #pragma unroll
     for (int e = 0; e < kMaxHd / 32; ++e)
-        if (lane + 32 * e < hd)
+        if (lane + 32 * e < hd && mine(lane + 32 * e))
             out[lane + 32 * e] = f_bf16(o[e] / l);
 }
 
 __global__ void __launch_bounds__(128) attn_rows(const AttnParams a)
 {
+    pdl_wait();
+    pdl_launch();
     __shared__ float qs[4][kMaxHd];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t rows = (int64_t)a.T * a.n_heads;
@@ -108,10 +102,445 @@ __global__ void __launch_bounds__(128) attn_rows(const AttnParams a)
         for (int d = lane; d < a.hd; d += 32)
             qs[warp][d] = bf16f(q[d]) * a.scale_log2;
         __syncwarp();
-        attend_row(a, t, h, qs[warp]);
+        attend_row(a, t, h, qs[warp], [](int) { return true; });
         __syncwarp();
     }
 }
+
+__device__ unsigned int g_timeouts;  // CTAs that gave up a wait
+
+// ---- tiles of rows ---------------------------------------------------------------
+// The (token, head) pairs of a KV head are the rows of tiles of 16 WM: a
+// group's heads and neighbouring tokens share every K and V row that is read.
+// A producer warp streams the visible K and V rows, 64 at a time, through a
+// ring of stages with TMA (swizzled; rows behind the last token and elements
+// behind head_dim read as 0); WM x WK warps take 16 rows each and a WK-th of
+// the stage's keys: scores, the running maximum and sum of the softmax, and
+// the weighted sum of V, all in registers (weights are rounded to bf16 for the
+// product with V, as tensor cores take them: 2^-9 of each; their sum is taken
+// before).  The warps that share rows merge through shared memory, the CTAs of
+// a cluster that share the keys of a tile through distributed shared memory,
+// in a fixed order.
+//
+// A masked weight is 0, and 0 times a NaN or infinity in a masked V row is
+// NaN.  So where a result is not finite its row is computed again by
+// attend_row, which touches visible rows alone.
+constexpr int kKeys = 64;  // of a stage
+
+struct TileParams {
+    CUtensorMap k, v;
+    AttnParams a;
+    int32_t rows;    // T * group
+    int32_t tiles, n_kv, split;
+};
+
+template <int HD, int WM, int WK>
+struct TileCfg {
+    static constexpr int ROWS = 16 * WM, KW = kKeys / WK;
+    static constexpr int WARPS = WM * WK, THREADS = 32 * (WARPS + 1);
+    static constexpr int STAGE = 2 * kKeys * HD * 2;
+    // two CTAs to an SM, but for the widest tiles of the widest heads
+    static constexpr int CTAS = HD == 128 && WM == 8 ? 1 : 2;
+    static constexpr int STAGES = (CTAS == 1 ? 192 : 96) * 1024 / STAGE;
+    static constexpr int OS = HD + 8;  // floats of a row of sums (padded)
+    static constexpr int SMEM = STAGES * STAGE + 1024;
+    static_assert(WK * ROWS * (OS + 2) * 4 + ROWS * 8 + WARPS * kMaxHd * 4 <= STAGES * STAGE,
+                  "the sums reuse the ring");
+};
+
+template <int HD, int WM, int WK>
+__global__ void __launch_bounds__(TileCfg<HD, WM, WK>::THREADS, (TileCfg<HD, WM, WK>::CTAS))
+    attn_tiles(const __grid_constant__ TileParams p)
+{
+    using C = TileCfg<HD, WM, WK>;
+    constexpr int KW = C::KW;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[2 * C::STAGES];
+    __shared__ int fail_flag, redo[C::ROWS];
+    volatile int *fail = &fail_flag;
+    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t bar0 = smem_u32(bars);
+    auto full = [&](int s) { return bar0 + 8 * s; };
+    auto empty = [&](int s) { return bar0 + 8 * (C::STAGES + s); };
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        fail_flag = 0;
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), C::WARPS);
+        }
+        mbar_init_fence();
+        prefetch_map(&p.k);
+        prefetch_map(&p.v);
+    }
+    for (int r = tid; r < C::ROWS; r += C::THREADS)
+        redo[r] = 0;
+    __syncthreads();
+    const AttnParams &a = p.a;
+    const int split = p.split, rank = blockIdx.x % split;
+    const int rest = blockIdx.x / split, kvh = rest % p.n_kv;
+    const int tile = p.tiles - 1 - rest / p.n_kv;  // the longest rows start first
+    const int r0 = tile * C::ROWS, nrows = min(C::ROWS, p.rows - r0);
+    const int pmin = a.pos + r0 / a.group, pmax = a.pos + (r0 + nrows - 1) / a.group;
+    // the keys that some row sees: [0, na) and [lo, pmax]
+    int na, lo;
+    visible(a, pmin, na, lo);
+    const int ta = (na + kKeys - 1) / kKeys, tn = ta + (pmax - lo + kKeys) / kKeys;
+    const int t0 = (int)((int64_t)tn * rank / split), t1 = (int)((int64_t)tn * (rank + 1) / split);
+    pdl_wait();
+    pdl_launch();
+    if (warp == C::WARPS) {
+        uint32_t ph = 1;
+        int s = 0;
+        bool ok = true;
+        int i = t0;
+        for (; i < t1; ++i) {
+            if (!warp_wait(empty(s), ph, fail)) {
+                ok = false;
+                break;
+            }
+            const int j0 = i < ta ? i * kKeys : lo + (i - ta) * kKeys;
+            const uint32_t ks = ring + s * C::STAGE, vs = ks + C::STAGE / 2;
+            if (elect_one()) {
+                mbar_expect_tx(full(s), C::STAGE);
+#pragma unroll
+                for (int d = 0; d < HD / 64; ++d)
+                    tma_3d(ks + d * kKeys * 128, &p.k, d * 64, j0, kvh, full(s));
+#pragma unroll
+                for (int d = 0; d < HD / 64; ++d)
+                    tma_3d(vs + d * kKeys * 128, &p.v, d * 64, j0, kvh, full(s));
+            }
+            __syncwarp();
+            if (++s == C::STAGES) {
+                s = 0;
+                ph ^= 1;
+            }
+        }
+        if (!ok && lane == 0)  // no copy may land after the CTA has gone
+            for (int j = max(t0, i - C::STAGES); j < i; ++j) {
+                const long long c0 = clock64();
+                while (!mbar_try_wait(full((j - t0) % C::STAGES), ((j - t0) / C::STAGES) & 1) &&
+                       clock64() - c0 < 2000000000ll) {
+                }
+            }
+    } else {
+        const int wm = warp % WM, wk = warp / WM, g = lane >> 2, t = lane & 3;
+        // rows g and g + 8 of the warp's 16
+        int prow[2];
+        uint32_t qf[HD / 16][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = r0 + wm * 16 + g + 8 * h;
+            const bool in = r < p.rows;
+            const int tok = in ? r / a.group : 0, hh = in ? r % a.group : 0;
+            prow[h] = in ? a.pos + tok : pmax;
+            const uint16_t *q = a.q + tok * a.q_ts + (kvh * a.group + hh) * a.q_hs;
+#pragma unroll
+            for (int i = 0; i < HD / 16; ++i)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int d = i * 16 + c * 8 + 2 * t;
+                    const uint32_t x0 = in && d < a.hd ? q[d] : 0;
+                    const uint32_t x1 = in && d + 1 < a.hd ? q[d + 1] : 0;
+                    qf[i][h + 2 * c] = x0 | (x1 << 16);
+                }
+        }
+        float o[HD / 8][4] = {}, m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        uint32_t ph = 0;
+        int s = 0;
+        for (int i = t0; i < t1; ++i) {
+            if (!warp_wait(full(s), ph, fail))
+                break;
+            const int j0 = (i < ta ? i * kKeys : lo + (i - ta) * kKeys) + wk * KW;
+            const uint32_t ks = ring + s * C::STAGE + wk * KW * 128, vs = ks + C::STAGE / 2;
+            float sc[KW / 8][4] = {};
+#pragma unroll
+            for (int d = 0; d < HD / 32; ++d)  // 32 elements of the heads at a time
+#pragma unroll
+                for (int n = 0; n < KW / 8; ++n) {
+                    const int row = n * 8 + (lane & 7), ch = (d & 1) * 4 + (lane >> 3);
+                    uint32_t b[4];
+                    ldmatrix4(b, ks + (d >> 1) * kKeys * 128 + row * 128 + ((ch ^ (row & 7)) << 4));
+                    mma_bf16(sc[n], qf[2 * d][0], qf[2 * d][1], qf[2 * d][2], qf[2 * d][3], b[0],
+                             b[1]);
+                    mma_bf16(sc[n], qf[2 * d + 1][0], qf[2 * d + 1][1], qf[2 * d + 1][2],
+                             qf[2 * d + 1][3], b[2], b[3]);
+                }
+#pragma unroll
+            for (int n = 0; n < KW / 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    sc[n][e] *= a.scale_log2;
+            const bool sink = i < ta;
+            if (sink ? j0 + KW > na : j0 + KW - 1 > pmin || (a.window && j0 <= pmax - a.window)) {
+#pragma unroll
+                for (int n = 0; n < KW / 8; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = j0 + n * 8 + 2 * t + (e & 1), pr = prow[e >> 1];
+                        const bool see = sink ? j < na
+                                              : j <= pr && (!a.window || j > pr - a.window ||
+                                                            j < a.sinks);
+                        if (!see)
+                            sc[n][e] = -INFINITY;
+                    }
+            }
+            float corr[2], base[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float mx = m[h];
+#pragma unroll
+                for (int n = 0; n < KW / 8; ++n)
+                    mx = fmaxf(mx, fmaxf(sc[n][2 * h], sc[n][2 * h + 1]));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                base[h] = mx == -INFINITY ? 0.f : mx;
+                corr[h] = ex2(m[h] - base[h]);
+                m[h] = mx;
+                l[h] *= corr[h];
+            }
+#pragma unroll
+            for (int n = 0; n < KW / 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    sc[n][e] = ex2(sc[n][e] - base[e >> 1]);
+                    l[e >> 1] += sc[n][e];
+                }
+            if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
+#pragma unroll
+                for (int d = 0; d < HD / 8; ++d)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        o[d][e] *= corr[e >> 1];
+            }
+#pragma unroll
+            for (int kk = 0; kk < KW / 16; ++kk) {
+                const uint32_t a0 = f2_bf16(sc[2 * kk][0], sc[2 * kk][1]);
+                const uint32_t a1 = f2_bf16(sc[2 * kk][2], sc[2 * kk][3]);
+                const uint32_t a2 = f2_bf16(sc[2 * kk + 1][0], sc[2 * kk + 1][1]);
+                const uint32_t a3 = f2_bf16(sc[2 * kk + 1][2], sc[2 * kk + 1][3]);
+#pragma unroll
+                for (int d = 0; d < HD / 16; ++d) {
+                    const int row = kk * 16 + (lane & 15), ch = (d & 3) * 2 + (lane >> 4);
+                    uint32_t b[4];
+                    ldmatrix4_t(b, vs + (d >> 2) * kKeys * 128 + row * 128 +
+                                       ((ch ^ (row & 7)) << 4));
+                    mma_bf16(o[2 * d], a0, a1, a2, a3, b[0], b[1]);
+                    mma_bf16(o[2 * d + 1], a0, a1, a2, a3, b[2], b[3]);
+                }
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(empty(s));
+            if (++s == C::STAGES) {
+                s = 0;
+                ph ^= 1;
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+        }
+        named_bar(1, C::WARPS * 32);  // every warp has read its last stage
+        float *os = reinterpret_cast<float *>(smem_raw + (ring - smem_u32(smem_raw)));
+        float *ml = os + WK * C::ROWS * C::OS;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = wk * C::ROWS + wm * 16 + g + 8 * h;
+#pragma unroll
+            for (int d = 0; d < HD / 8; ++d)
+                *reinterpret_cast<float2 *>(os + r * C::OS + d * 8 + 2 * t) =
+                    make_float2(o[d][2 * h], o[d][2 * h + 1]);
+            if (t == 0) {
+                ml[2 * r] = m[h];
+                ml[2 * r + 1] = l[h];
+            }
+        }
+        named_bar(1, C::WARPS * 32);
+    }
+    // merge: over the warps of a row, then over the cluster's CTAs
+    float *os = reinterpret_cast<float *>(smem_raw + (ring - smem_u32(smem_raw)));
+    float *ml = os + WK * C::ROWS * C::OS, *mc = ml + 2 * WK * C::ROWS;
+    const int hd = a.hd, nt = C::WARPS * 32;
+    auto weigh = [](float m, float M) { return m == -INFINITY ? 0.f : ex2(m - M); };
+    auto put = [&](int r, int d, float v) {
+        if (!(fabsf(v) < INFINITY)) {
+            redo[r] = 1;
+            return;
+        }
+        const int row = r0 + r;
+        a.out[(row / a.group) * a.o_ts + (kvh * a.group + row % a.group) * a.o_hs + d] = f_bf16(v);
+    };
+    if (split == 1) {
+        if (tid < nt && !*fail)
+            for (int i = tid; i < nrows * hd; i += nt) {
+                const int r = i / hd, d = i - r * hd;
+                float M = -INFINITY, L = 0.f, O = 0.f;
+#pragma unroll
+                for (int k = 0; k < WK; ++k)
+                    M = fmaxf(M, ml[2 * (k * C::ROWS + r)]);
+#pragma unroll
+                for (int k = 0; k < WK; ++k) {
+                    const int at = k * C::ROWS + r;
+                    const float w = weigh(ml[2 * at], M);
+                    L = fmaf(ml[2 * at + 1], w, L);
+                    O = fmaf(os[at * C::OS + d], w, O);
+                }
+                put(r, d, O / L);
+            }
+        __syncthreads();
+    } else {
+        if (tid < nt) {
+            for (int i = tid; i < nrows * hd; i += nt) {
+                const int r = i / hd, d = i - r * hd;
+                float M = -INFINITY, L = 0.f, O = 0.f;
+#pragma unroll
+                for (int k = 0; k < WK; ++k)
+                    M = fmaxf(M, ml[2 * (k * C::ROWS + r)]);
+#pragma unroll
+                for (int k = 0; k < WK; ++k) {
+                    const int at = k * C::ROWS + r;
+                    const float w = weigh(ml[2 * at], M);
+                    L = fmaf(ml[2 * at + 1], w, L);
+                    O = fmaf(os[at * C::OS + d], w, O);
+                }
+                os[r * C::OS + d] = O;
+                if (d == 0) {
+                    mc[2 * r] = M;
+                    mc[2 * r + 1] = L;
+                }
+            }
+        }
+        cluster_sync();
+        if (tid < nt && !*fail) {
+            const uint32_t oa = smem_u32(os), ma = smem_u32(mc);
+            for (int i = rank * nt + tid; i < nrows * hd; i += split * nt) {
+                const int r = i / hd, d = i - r * hd;
+                float M = -INFINITY, L = 0.f, O = 0.f;
+                for (int k0 = 0; k0 < split; k0 += 4) {  // four CTAs' partials at a time
+                    float mk[4], lk[4], ok[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const bool in = k0 + k < split;
+                        const int kk = in ? k0 + k : 0;
+                        const float x = ld_cluster(map_rank(ma + r * 8, kk));
+                        mk[k] = in ? x : -INFINITY;
+                        lk[k] = ld_cluster(map_rank(ma + r * 8 + 4, kk));
+                        ok[k] = ld_cluster(map_rank(oa + (r * C::OS + d) * 4, kk));
+                    }
+                    float Mn = M;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        Mn = fmaxf(Mn, mk[k]);
+                    const float c = weigh(M, Mn);
+                    L *= c;
+                    O *= c;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float w = weigh(mk[k], Mn);
+                        L = fmaf(lk[k], w, L);
+                        O = fmaf(ok[k], w, O);
+                    }
+                    M = Mn;
+                }
+                put(r, d, O / L);
+            }
+        }
+        cluster_sync();  // no CTA leaves, or writes below, while another reads
+    }
+    if (warp < C::WARPS) {
+        float *qs = mc + 2 * C::ROWS + warp * kMaxHd;
+        for (int r = warp; r < nrows; r += C::WARPS)
+            if (redo[r]) {
+                const int row = r0 + r, tok = row / a.group, h = kvh * a.group + row % a.group;
+                const uint16_t *q = a.q + tok * a.q_ts + h * a.q_hs;
+                for (int d = lane; d < hd; d += 32)
+                    qs[d] = bf16f(q[d]) * a.scale_log2;
+                __syncwarp();
+                attend_row(a, tok, h, qs, [&](int d) {  // this CTA's share of the row
+                    return ((r * hd + d) / nt) % split == rank;
+                });
+                __syncwarp();
+            }
+    }
+    if (tid == 0 && *fail)
+        atomicAdd(&g_timeouts, 1u);
+}
+
+template <int HD, int WM, int WK>
+cudaError_t launch_tiles(TileParams &p, cudaStream_t stream)
+{
+    using C = TileCfg<HD, WM, WK>;
+    p.tiles = (p.rows + C::ROWS - 1) / C::ROWS;
+    const AttnParams &a = p.a;
+    // keys of the longest tile, in stages; the CTAs of a cluster share them, as
+    // many as run at once and have two stages to read
+    const int last = a.pos + a.T - 1, first = a.pos + (p.tiles - 1) * C::ROWS / a.group;
+    const int lo = a.window && first - a.window + 1 > 0 ? first - a.window + 1 : 0;
+    const int sinks = a.sinks < lo ? a.sinks : lo;
+    const int64_t stages = (sinks + kKeys - 1) / kKeys + ((int64_t)last - lo + kKeys) / kKeys;
+    const int64_t base = (int64_t)p.tiles * p.n_kv, room = (int64_t)sm_count() * C::CTAS;
+    p.split = 1;
+    while (p.split < 16 && base * p.split * 2 <= room && stages >= 4 * p.split)
+        p.split *= 2;
+    if (base * p.split > INT32_MAX)
+        return cudaErrorInvalidValue;
+    auto kernel = attn_tiles<HD, WM, WK>;
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e =
+        allow_once(allowed, reinterpret_cast<const void *>(kernel), C::SMEM, true);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(base * p.split));
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int HD>
+cudaError_t launch_hd(TileParams &p, cudaStream_t stream)
+{
+    const int64_t wide = (int64_t)((p.rows + 127) / 128) * p.n_kv;
+    if (p.rows <= 16)
+        return launch_tiles<HD, 1, 4>(p, stream);
+    if (p.rows <= 32)
+        return launch_tiles<HD, 2, 2>(p, stream);
+    if (wide < sm_count())
+        return launch_tiles<HD, 4, 1>(p, stream);
+    return launch_tiles<HD, 8, 1>(p, stream);
+}
+
+// Whether TMA can read the cache rows: 16-byte strides and bases.
+bool fits_tiles(const amk_attention_args *a)
+{
+    auto rows = [&](const void *p, int64_t rs, int64_t hs) {
+        return aligned(p, 16) && rs % 8 == 0 && rs >= a->head_dim &&
+               (a->n_kv_heads == 1 || (hs % 8 == 0 && hs >= a->head_dim));
+    };
+    return a->head_dim <= 128 && (int64_t)a->n_tokens * (a->n_heads / a->n_kv_heads) < (1 << 28) &&
+           rows(a->k, a->k_row_stride, a->k_head_stride) &&
+           rows(a->v, a->v_row_stride, a->v_head_stride);
+}
+
+}  // namespace
+
+cudaError_t timeouts_attention(uint32_t *n)
+{
+    return cudaMemcpyFromSymbol(n, g_timeouts, sizeof *n);
+}
+
+namespace {
 
 int check_attention(const amk_attention_args *a)
 {
@@ -182,8 +611,30 @@ extern "C" int amk_attention(const amk_attention_args *a, void *cuda_stream)
     p.window = a->window;
     p.sinks = a->sinks;
     p.scale_log2 = (a->scale > 0.f ? a->scale : 1.f / sqrtf((float)a->head_dim)) * 1.4426950408889634f;
+    if (!sm_count())
+        return no_device("amk_attention");
+    cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+    if (fits_tiles(a)) {
+        TileParams t;
+        t.a = p;
+        t.rows = a->n_tokens * p.group;
+        t.n_kv = a->n_kv_heads;
+        const int64_t rows = (int64_t)a->pos + a->n_tokens;  // what lies behind them reads as 0
+        auto map = [&](CUtensorMap *m, const void *base, int64_t rs, int64_t hs) {
+            return encode_3d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, a->head_dim, rows,
+                             a->n_kv_heads, 2 * rs, 2 * (a->n_kv_heads == 1 ? rs : hs), 64, kKeys,
+                             CU_TENSOR_MAP_SWIZZLE_128B);
+        };
+        if (!map(&t.k, a->k, a->k_row_stride, a->k_head_stride) ||
+            !map(&t.v, a->v, a->v_row_stride, a->v_head_stride))
+            return amk_set_error(AMK_ERR_CUDA, "amk_attention: a tensor map was refused");
+        return launch_status(a->head_dim <= 64 ? launch_hd<64>(t, st) : launch_hd<128>(t, st),
+                             "amk_attention");
+    }
     const int64_t rows = (int64_t)a->n_tokens * a->n_heads;
-    const unsigned grid = (unsigned)((rows + 3) / 4 < (1 << 20) ? (rows + 3) / 4 : (1 << 20));
-    attn_rows<<<grid, 128, 0, static_cast<cudaStream_t>(cuda_stream)>>>(p);
-    return launch_status(cudaGetLastError(), "amk_attention");
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((rows + 3) / 4 < (1 << 20) ? (rows + 3) / 4 : (1 << 20)));
+    cfg.blockDim = dim3(128);
+    cfg.stream = st;
+    return launch_status(cudaLaunchKernelEx(&cfg, attn_rows, p), "amk_attention");
 }

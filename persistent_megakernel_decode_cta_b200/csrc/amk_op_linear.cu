@@ -200,55 +200,6 @@ int check_linear(const amk_linear_args *a)
 
 // ---- the tensor-core kernel ----------------------------------------------------
 
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                 const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                 const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_fn()
-{
-    static std::atomic<EncodeTiled> fn{nullptr};
-    EncodeTiled f = fn.load(std::memory_order_relaxed);
-    if (!f) {
-        void *sym = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &sym, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess) {
-            f = reinterpret_cast<EncodeTiled>(sym);
-            fn.store(f, std::memory_order_relaxed);
-        }
-        cudaGetLastError();
-    }
-    return f;
-}
-
-// Map of `rows` rows of `inner` elements, `pitch` bytes apart, in boxes of
-// box_inner x box_rows.
-bool encode(CUtensorMap *map, CUtensorMapDataType type, const void *base, int64_t inner,
-            int64_t rows, int64_t pitch, int box_inner, int box_rows, CUtensorMapSwizzle swizzle)
-{
-    const EncodeTiled f = encode_fn();
-    const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)pitch};
-    const cuuint32_t box[2] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows}, one[2] = {1, 1};
-    return f && f(map, type, 2, const_cast<void *>(base), dims, strides, box, one,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-int sm_count()
-{
-    static std::atomic<int> sms[64];
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
-        return 0;
-    n = sms[dev].load(std::memory_order_relaxed);
-    if (!n && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
-        sms[dev].store(n, std::memory_order_relaxed);
-    return n;
-}
-
 bool fits_tensor_cores(const amk_linear_args *a)
 {
     const int64_t row = a->quant == AMK_QUANT_BF16    ? 2 * (int64_t)a->k
@@ -345,11 +296,8 @@ int launch_few(const amk_linear_args *a, const Epilogue &e, cudaStream_t stream)
 int launch_tc(const amk_linear_args *a, const Epilogue &e, cudaStream_t stream)
 {
     const int sms = sm_count();
-    if (!sms) {
-        int n = 0;
-        const cudaError_t err = cudaGetDeviceCount(&n);
-        return launch_status(err == cudaSuccess ? cudaErrorNoDevice : err, "amk_linear");
-    }
+    if (!sms)
+        return no_device("amk_linear");
     const Choice c = choose(a, sms);
     TcParams p;
     p.e = e;
@@ -367,18 +315,18 @@ int launch_tc(const amk_linear_args *a, const Epilogue &e, cudaStream_t stream)
     p.tiles_m = (int)(((int64_t)a->m + c.v.nt - 1) / c.v.nt);
     p.tiles = (int)(((int64_t)a->n + rows - 1) / rows) * p.tiles_m;
     p.split = c.split;
-    bool ok = encode(&p.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a->x, a->k, a->m,
+    bool ok = encode_2d(&p.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a->x, a->k, a->m,
                      a->m == 1 ? (2 * (int64_t)a->k + 15) & ~(int64_t)15 : 2 * a->ldx, 64, c.v.nt,
                      CU_TENSOR_MAP_SWIZZLE_128B);
     for (int i = 0; i < (a->up ? 2 : 1) && ok; ++i) {
         CUtensorMap *map = i ? &p.up : &p.w;
         const void *w = i ? a->up : a->w;
         if (a->quant == AMK_QUANT_BF16)
-            ok = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, w, a->k, a->n, 2 * (int64_t)a->k, 64,
+            ok = encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, w, a->k, a->n, 2 * (int64_t)a->k, 64,
                         rows, CU_TENSOR_MAP_SWIZZLE_128B);
         else {
             const int per = a->quant == AMK_QUANT_W8A16 ? 1 : 2;  // codes to a byte
-            ok = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, a->k / per, a->n, a->k / per,
+            ok = encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, a->k / per, a->n, a->k / per,
                         ksub * 64 / per, rows, CU_TENSOR_MAP_SWIZZLE_NONE);
         }
     }

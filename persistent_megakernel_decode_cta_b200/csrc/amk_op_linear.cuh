@@ -626,19 +626,10 @@ cudaError_t launch_one(const TcParams &p, int grid, cudaStream_t stream)
 {
     using C = Cfg<QUANT, NT, SPLIT, PROMOTE>;
     auto kernel = linear_tc<QUANT, NT, SPLIT, PROMOTE>;
-    // the shared memory is allowed once per device (by whichever thread comes first)
     static std::atomic<uint64_t> allowed{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = allow_once(allowed, reinterpret_cast<const void *>(kernel), C::SMEM);
     if (e != cudaSuccess)
         return e;
-    if (dev >= 64 || !(allowed.load(std::memory_order_relaxed) >> dev & 1)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-        if (e != cudaSuccess)
-            return e;
-        if (dev < 64)
-            allowed.fetch_or(1ull << dev, std::memory_order_relaxed);
-    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(C::THREADS);

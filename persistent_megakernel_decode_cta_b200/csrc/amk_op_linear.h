@@ -59,10 +59,6 @@ cudaError_t skinny_int4(const SkinnyParams &p, cudaStream_t stream);
 cudaError_t launch_bf16(const Variant &v, const TcParams &p, int grid, cudaStream_t stream);
 cudaError_t launch_int8(const Variant &v, const TcParams &p, int grid, cudaStream_t stream);
 cudaError_t launch_int4(const Variant &v, const TcParams &p, int grid, cudaStream_t stream);
-// CTAs of these kernels that gave up a wait on the current device.
-cudaError_t timeouts_bf16(uint32_t *n);
-cudaError_t timeouts_int8(uint32_t *n);
-cudaError_t timeouts_int4(uint32_t *n);
 
 }  // namespace linear
 }  // namespace amk

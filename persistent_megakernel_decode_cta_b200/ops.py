@@ -10,77 +10,108 @@ would have to record a gradient is refused.
 from __future__ import annotations
 
 import ctypes
-from typing import Optional, Tuple
+from typing import Optional
 
 from . import AmkError, _check, abi
 
 _I32 = 2**31 - 1
 _INVALID = abi.ERR["AMK_ERR_INVALID_ARG"]
+_pack_linear = abi.packer(abi.LinearArgs)
+_pack_attention = abi.packer(abi.AttentionArgs)
+_pack_verify = abi.packer(abi.VerifyArgs)
 _torch = None
+_lib = _raw_stream = _device = None
 
 
-def _lib():
-    """torch and the loaded library (both are imported on the first call)."""
-    global _torch
-    if _torch is None:
-        import torch
-        _torch = torch
-    return _torch, abi.lib()
+def _load():
+    """Imports torch and loads the library, on the first call."""
+    global _torch, _lib, _raw_stream, _device
+    import torch
+    _lib = abi.lib()
+    # the current stream's handle and device without the objects around them
+    # (which cost more than the launch), where this torch has them
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda i: torch.cuda.current_stream(i).cuda_stream)
+    _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _torch = torch
 
 
 def _refuse(what: str):
     raise AmkError(_INVALID, what)
 
 
-def _tensors(what: str, stream, named):
-    """Checks that every tensor is on one CUDA device and needs no gradient;
-    returns the device index and the stream handle."""
-    torch = _torch
-    dev = None
-    grad = torch.is_grad_enabled()
-    for name, t in named:
+def _check_tensors(what: str, names, tensors) -> int:
+    """The CUDA device that all of the tensors (or None) are on; refuses others
+    and any that a gradient would have to be recorded for."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and (t.get_device() != dev or dev < 0):
+            break
+    else:
+        if not _torch.is_grad_enabled():
+            return dev
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                break
+        else:
+            return dev
+    for name, t in zip(names, tensors):
         if t is None:
             continue
         if not t.is_cuda:
             _refuse(f"{what}: {name} is not a CUDA tensor")
-        i = t.get_device()
-        if dev is None:
-            dev = i
-        elif i != dev:
-            _refuse(f"{what}: {name} is on cuda:{i}, others on cuda:{dev}")
-        if grad and t.requires_grad:
+        if t.get_device() != dev:
+            _refuse(f"{what}: {name} is on cuda:{t.get_device()}, others on cuda:{dev}")
+        if t.requires_grad:
             _refuse(f"{what}: {name} requires a gradient, which is not computed")
+    _refuse(f"{what}: tensors are on no one CUDA device")
+
+
+def _launch(what: str, fn, args: bytes, dev: int, stream, tensors):
     if stream is None:
-        return dev, torch.cuda.current_stream(dev).cuda_stream
-    side = torch.cuda.ExternalStream(stream, device=dev)
-    for _, t in named:
-        if t is not None:
-            t.record_stream(side)
-    return dev, stream
-
-
-def _call(fn, args, dev: int, stream: int, what: str):
-    torch = _torch
-    if dev == torch.cuda.current_device():
-        rc = fn(ctypes.byref(args), stream)
+        st = _raw_stream(dev)
     else:
-        with torch.cuda.device(dev):
-            rc = fn(ctypes.byref(args), stream)
+        st = stream
+        side = _torch.cuda.ExternalStream(stream, device=dev)
+        for t in tensors:  # their memory is not reused before this stream is through
+            if t is not None:
+                t.record_stream(side)
+    if dev == _device():
+        rc = fn(args, st)
+    else:
+        with _torch.cuda.device(dev):
+            rc = fn(args, st)
     if rc != abi.AMK_OK:
         _check(rc, what)
 
 
-def _new(what, stream, shape, dtype, dev):
-    """A result tensor, from the pool of the stream that will write it."""
-    torch = _torch
+def _new(like, stream, shape, dtype):
+    """A result on the device of `like`, from the pool of the stream that will
+    write it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=f"cuda:{dev}")
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev)):
-        return torch.empty(shape, dtype=dtype, device=f"cuda:{dev}")
+        return like.new_empty(shape, dtype=dtype)
+    side = _torch.cuda.ExternalStream(stream, device=like.device)
+    with _torch.cuda.stream(side):
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _rows(what: str, name: str, t, n: int):
+    """(rows, row stride) of a tensor seen as [rows][n]."""
+    if t.dim() == 2:
+        ld, one = t.stride()
+        if one == 1 or n == 1:
+            rows = t.shape[0]
+            if rows <= 1:
+                return rows, n
+            if ld < n:
+                _refuse(f"{what}: the rows of {name} overlap")
+            return rows, ld
+    if t.is_contiguous():
+        return (t.numel() // n if n else 0), n
+    _refuse(f"{what}: {name} is neither contiguous nor a matrix of contiguous rows")
+
+
+_LINEAR = ("x", "w", "scale", "bias", "up", "up_scale", "up_bias", "residual", "out")
 
 
 def linear(x, w, *, scale=None, bias=None, act: str = "none", up=None, up_scale=None,
@@ -95,95 +126,88 @@ def linear(x, w, *, scale=None, bias=None, act: str = "none", up=None, up_scale=
     residual: bf16 or fp32 [..., n].  Returns bf16 or fp32 [..., n]: ``out``
     (which may be ``residual``), else a new tensor of ``out_dtype`` (default:
     bf16)."""
-    torch, lib = _lib()
-    dev, st = _tensors("linear", stream,
-                       (("x", x), ("w", w), ("scale", scale), ("bias", bias), ("up", up),
-                        ("up_scale", up_scale), ("up_bias", up_bias), ("residual", residual),
-                        ("out", out)))
+    if _torch is None:
+        _load()
+    torch = _torch
+    dev = _check_tensors("linear", _LINEAR, (x, w, scale, bias, up, up_scale, up_bias, residual,
+                                             out))
     bf16, f32 = torch.bfloat16, torch.float32
     if x.dtype is not bf16:
         _refuse(f"linear: x is {x.dtype}, not bfloat16")
     if x.dim() < 1 or w.dim() != 2:
         _refuse("linear: x needs one dimension at least and w two")
-    if act not in abi.ACT:
+    act_code = abi.ACT.get(act)
+    if act_code is None:
         _refuse(f"linear: unknown activation {act!r}")
-    k = x.shape[-1]
+    xs = x.shape
+    k = xs[-1]
     n = w.shape[0]
     wt = w.dtype
     if wt is bf16:
-        quant, cols, sshape = abi.QUANT_BF16, k, None
+        quant, cols, sshape = 0, k, None
     elif wt is torch.int8:
-        quant, cols, sshape = abi.QUANT_W8A16, k, (n,)
+        quant, cols, sshape = 1, k, (n,)
     elif wt is torch.uint8:
-        quant, cols, sshape = abi.QUANT_W4A16, k // 2, (n, (k + 127) // 128)
         if k % 2:
             _refuse("linear: int4 rows need an even number of inputs")
+        quant, cols, sshape = 2, k // 2, (n, (k + 127) // 128)
     else:
         _refuse(f"linear: no weight format with {wt} elements")
-    for name, m, s in (("w", w, scale), ("up", up, up_scale)):
-        if m is None:
-            if s is not None:
-                _refuse(f"linear: {name}_scale without {name}")
-            continue
-        if m.dtype is not wt or m.shape != (n, cols) or not m.is_contiguous():
-            _refuse(f"linear: {name} is not a contiguous {wt} [{n}, {cols}] matrix")
-        if sshape is None:
-            if s is not None:
-                _refuse(f"linear: bf16 {name} takes no scale")
-        elif s is None or s.dtype is not torch.float16 or s.shape != sshape or \
-                not s.is_contiguous():
-            _refuse(f"linear: the scale of {name} is not contiguous float16 {list(sshape)}")
-    if up is None and up_bias is not None:
-        _refuse("linear: up_bias without up")
-    for name, b in (("bias", bias), ("up_bias", up_bias)):
+    _check_weights("w", w, scale, wt, (n, cols), sshape)
+    if up is not None:
+        _check_weights("up", up, up_scale, wt, (n, cols), sshape)
+    elif up_scale is not None or up_bias is not None:
+        _refuse("linear: up_scale or up_bias without up")
+    for b in (bias, up_bias):
         if b is not None and (b.dtype is not bf16 or b.shape != (n,) or not b.is_contiguous()):
-            _refuse(f"linear: {name} is not contiguous bfloat16 [{n}]")
-    lead = x.shape[:-1]
-    shape = (*lead, n)
-    m, ldx = _rows("linear", "x", x)
+            _refuse(f"linear: a bias is not contiguous bfloat16 [{n}]")
+    m, ldx = _rows("linear", "x", x, k)
+    shape = (m, n) if len(xs) == 2 else (*xs[:-1], n)
     if out is None:
-        out = _new("linear", stream, shape, out_dtype or bf16, dev)
-    elif out_dtype is not None and out.dtype is not out_dtype:
-        _refuse(f"linear: out is {out.dtype}, not {out_dtype}")
+        out = _new(x, stream, shape, out_dtype or bf16)
+        ldy = n
+    else:
+        if out.shape != shape:
+            _refuse(f"linear: out has shape {list(out.shape)}, not {list(shape)}")
+        if out_dtype is not None and out.dtype is not out_dtype:
+            _refuse(f"linear: out is {out.dtype}, not {out_dtype}")
+        _, ldy = _rows("linear", "out", out, n)
     ot = out.dtype
     if ot is not bf16 and ot is not f32:
         _refuse(f"linear: out is {ot}, not bfloat16 or float32")
-    if out.shape != shape:
-        _refuse(f"linear: out has shape {list(out.shape)}, not {list(shape)}")
-    _, ldy = _rows("linear", "out", out)
-    ldr, rt = 0, 0
+    ldr = rt = rp = 0
     if residual is not None:
-        if residual.dtype is not bf16 and residual.dtype is not f32:
-            _refuse(f"linear: residual is {residual.dtype}, not bfloat16 or float32")
+        rd = residual.dtype
+        if rd is not bf16 and rd is not f32:
+            _refuse(f"linear: residual is {rd}, not bfloat16 or float32")
         if residual.shape != shape:
             _refuse(f"linear: residual has shape {list(residual.shape)}, not {list(shape)}")
-        _, ldr = _rows("linear", "residual", residual)
-        rt = abi.DT_F32 if residual.dtype is f32 else abi.DT_BF16
+        _, ldr = _rows("linear", "residual", residual, n)
+        rt = 1 if rd is f32 else 0
+        rp = residual.data_ptr()
     if m == 0:
         return out
-    if max(m, n, k) > _I32:
+    if m > _I32 or n > _I32 or k > _I32:
         _refuse("linear: a size above 2^31 - 1")
-    a = abi.LinearArgs(x.data_ptr(), w.data_ptr(), _ptr(scale), _ptr(bias), _ptr(up),
-                       _ptr(up_scale), _ptr(up_bias), _ptr(residual), out.data_ptr(), ldx, ldr,
-                       ldy, m, n, k, quant, abi.ACT[act], rt,
-                       abi.DT_F32 if ot is f32 else abi.DT_BF16)
-    _call(lib.amk_linear, a, dev, st, "amk_linear")
+    args = _pack_linear(
+        x.data_ptr(), w.data_ptr(), scale.data_ptr() if scale is not None else 0,
+        bias.data_ptr() if bias is not None else 0, up.data_ptr() if up is not None else 0,
+        up_scale.data_ptr() if up_scale is not None else 0,
+        up_bias.data_ptr() if up_bias is not None else 0, rp, out.data_ptr(), ldx, ldr, ldy, m, n,
+        k, quant, act_code, rt, 1 if ot is f32 else 0)
+    _launch("amk_linear", _lib.amk_linear, args, dev, stream,
+            (x, w, scale, bias, up, up_scale, up_bias, residual, out))
     return out
 
 
-def _rows(what: str, name: str, t) -> Tuple[int, int]:
-    """(rows, row stride) of a tensor seen as [rows][last dimension]."""
-    n = t.shape[-1]
-    if t.dim() == 2 and (t.stride(1) == 1 or n == 1):
-        rows, ld = t.shape[0], t.stride(0)
-        if rows <= 1:
-            ld = max(ld, n)
-        elif ld < n:
-            _refuse(f"{what}: the rows of {name} overlap")
-        return rows, ld
-    if t.is_contiguous():
-        return (t.numel() // n if n else 0), n
-    _refuse(f"{what}: {name} is neither contiguous nor a matrix of contiguous rows")
+def _check_weights(name, m, s, dtype, shape, sshape):
+    if m.dtype is not dtype or m.shape != shape or not m.is_contiguous():
+        _refuse(f"linear: {name} is not a contiguous {dtype} {list(shape)} matrix")
+    if sshape is None:
+        if s is not None:
+            _refuse(f"linear: bf16 {name} takes no scale")
+    elif s is None or s.dtype is not _torch.float16 or s.shape != sshape or not s.is_contiguous():
+        _refuse(f"linear: the scale of {name} is not contiguous float16 {list(sshape)}")
 
 
 def attention(q, k, v, pos: int, *, window: int = 0, sinks: int = 0,
@@ -195,24 +219,28 @@ def attention(q, k, v, pos: int, *, window: int = 0, sinks: int = 0,
     up to its own, and to the first ``sinks`` rows.  scale: default
     1 / sqrt(head_dim).  Returns bf16 [tokens, heads, head_dim] (``out`` if
     given).  Leading dimensions may be strided; head_dim is contiguous."""
-    torch, lib = _lib()
-    dev, st = _tensors("attention", stream, (("q", q), ("k", k), ("v", v), ("out", out)))
-    bf16 = torch.bfloat16
+    if _torch is None:
+        _load()
+    dev = _check_tensors("attention", ("q", "k", "v", "out"), (q, k, v, out))
+    bf16 = _torch.bfloat16
     if q.dtype is not bf16 or k.dtype is not bf16 or v.dtype is not bf16:
         _refuse("attention: q, k and v must be bfloat16")
-    if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape or k.shape[2] != q.shape[2]:
+    qs, ks = q.shape, k.shape
+    if len(qs) != 3 or len(ks) != 3 or ks != v.shape or ks[2] != qs[2]:
         _refuse("attention: q must be [tokens, heads, head_dim], k and v [kv_heads, rows, head_dim]")
-    T, nh, hd = q.shape
-    nkv, rows, _ = k.shape
+    T, nh, hd = qs
+    nkv, rows, _ = ks
     if out is None:
-        out = _new("attention", stream, (T, nh, hd), bf16, dev)
-    elif out.dtype is not bf16 or out.shape != q.shape:
+        out = _new(q, stream, qs, bf16)
+    elif out.dtype is not bf16 or out.shape != qs:
         _refuse("attention: out must be bfloat16 of q's shape")
     (qt, qh, q1), (kh, kr, k1), (vh, vr, v1), (ot, oh, o1) = (q.stride(), k.stride(), v.stride(),
                                                               out.stride())
     if hd > 1 and not q1 == k1 == v1 == o1 == 1:
         _refuse("attention: head_dim must be contiguous")
-    if scale is not None and not 0 < scale < float("inf"):
+    if scale is None:
+        scale = 0.0
+    elif not 0 < scale < float("inf"):
         _refuse("attention: scale must be positive and finite")
     if not 0 <= pos <= rows - T or rows > _I32:
         raise AmkError(abi.ERR["AMK_ERR_POS_RANGE"], f"attention: positions {pos} .. "
@@ -221,10 +249,11 @@ def attention(q, k, v, pos: int, *, window: int = 0, sinks: int = 0,
         _refuse("attention: window or sinks < 0")
     if T == 0:
         return out
-    window, sinks = min(window, _I32), min(sinks, _I32)  # beyond any position: the same mask
-    a = abi.AttentionArgs(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), qt, qh, ot, oh,
-                          kh, kr, vh, vr, T, pos, nh, nkv, hd, rows, window, sinks, scale or 0.0)
-    _call(lib.amk_attention, a, dev, st, "amk_attention")
+    args = _pack_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), qt, qh, ot, oh,
+                           kh, kr, vh, vr, T, pos, nh, nkv, hd, rows,
+                           # beyond any position: the same mask
+                           min(window, _I32), min(sinks, _I32), scale)
+    _launch("amk_attention", _lib.amk_attention, args, dev, stream, (q, k, v, out))
     return out
 
 
@@ -238,37 +267,56 @@ def verify_draft(target_logits, draft_tokens, u, *, draft_logits=None, temperatu
     distribution.  temperature 0 is greedy.  Returns (tokens int32
     [drafts + 1], n_accepted int32 [1]) on the device: the accepted tokens, the
     drawn one, then -1.  With no drafts it samples one token."""
-    torch, lib = _lib()
-    dev, st = _tensors("verify_draft", stream,
-                       (("target_logits", target_logits), ("draft_tokens", draft_tokens),
-                        ("u", u), ("draft_logits", draft_logits), ("tokens", tokens),
-                        ("n_accepted", n_accepted)))
-    if target_logits.dim() != 2 or target_logits.shape[0] < 1:
+    if _torch is None:
+        _load()
+    torch = _torch
+    dev = _check_tensors("verify_draft", ("target_logits", "draft_tokens", "u", "draft_logits",
+                                          "tokens", "n_accepted"),
+                         (target_logits, draft_tokens, u, draft_logits, tokens, n_accepted))
+    f32, i32 = torch.float32, torch.int32
+    ts = target_logits.shape
+    if len(ts) != 2 or ts[0] < 1:
         _refuse("verify_draft: target_logits must be [drafts + 1, vocab]")
-    d, vocab = target_logits.shape[0] - 1, target_logits.shape[1]
+    d, vocab = ts[0] - 1, ts[1]
     if vocab > _I32 or d > _I32:
         _refuse("verify_draft: a size above 2^31 - 1")
-    f32, i32 = torch.float32, torch.int32
-    if tokens is None:
-        tokens = _new("verify_draft", stream, (d + 1,), i32, dev)
-    if n_accepted is None:
-        n_accepted = _new("verify_draft", stream, (1,), i32, dev)
-    for name, t, dtype, shape in (("draft_tokens", draft_tokens, i32, (d,)), ("u", u, f32, (d + 1,)),
-                                  ("tokens", tokens, i32, (d + 1,)),
-                                  ("n_accepted", n_accepted, i32, (1,))):
-        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-            _refuse(f"verify_draft: {name} is not contiguous {dtype} {list(shape)}")
-    for name, t, n in (("target_logits", target_logits, d + 1), ("draft_logits", draft_logits, d)):
-        if t is not None and (t.dtype is not f32 or t.shape != (n, vocab)
-                              or (vocab > 1 and t.stride(1) != 1)):
-            _refuse(f"verify_draft: {name} is not float32 [{n}, {vocab}] with contiguous rows")
-    nbytes = lib.amk_verify_workspace(d, vocab)
+    nbytes = _lib.amk_verify_workspace(d, vocab)
     if nbytes < 0:
         _check(int(nbytes), "amk_verify_workspace")
-    ws = _new("verify_draft", stream, (nbytes,), torch.uint8, dev)
-    a = abi.VerifyArgs(target_logits.data_ptr(), _ptr(draft_logits) or None, u.data_ptr(),
-                       draft_tokens.data_ptr() or None, tokens.data_ptr(), n_accepted.data_ptr(),
-                       target_logits.stride(0), draft_logits.stride(0) if draft_logits is not None
-                       else 0, d, vocab, temperature, ws.data_ptr(), nbytes)
-    _call(lib.amk_verify_draft, a, dev, st, "amk_verify_draft")
+    if draft_tokens.dtype is not i32 or draft_tokens.shape != (d,) or \
+            not draft_tokens.is_contiguous():
+        _refuse(f"verify_draft: draft_tokens is not contiguous int32 [{d}]")
+    if u.dtype is not f32 or u.shape != (d + 1,) or not u.is_contiguous():
+        _refuse(f"verify_draft: u is not contiguous float32 [{d + 1}]")
+    tstr, one = target_logits.stride()
+    if target_logits.dtype is not f32 or (one != 1 and vocab > 1):
+        _refuse("verify_draft: target_logits is not float32 with contiguous rows")
+    dstr = dp = 0
+    if draft_logits is not None:
+        if draft_logits.dtype is not f32 or draft_logits.shape != (d, vocab) or \
+                (draft_logits.stride(1) != 1 and vocab > 1):
+            _refuse(f"verify_draft: draft_logits is not float32 [{d}, {vocab}] with contiguous rows")
+        dstr, dp = draft_logits.stride(0), draft_logits.data_ptr()
+    if tokens is None:
+        tokens = _new(u, stream, (d + 1,), i32)
+    elif tokens.dtype is not i32 or tokens.shape != (d + 1,) or not tokens.is_contiguous():
+        _refuse(f"verify_draft: tokens is not contiguous int32 [{d + 1}]")
+    if n_accepted is None:
+        n_accepted = _new(u, stream, (1,), i32)
+    elif n_accepted.dtype is not i32 or n_accepted.shape != (1,):
+        _refuse("verify_draft: n_accepted is not int32 [1]")
+    work = _new(u, stream, (nbytes,), torch.uint8)
+    args = _pack_verify(target_logits.data_ptr(), dp, u.data_ptr(), draft_tokens.data_ptr(),
+                        tokens.data_ptr(), n_accepted.data_ptr(), tstr, dstr, d, vocab,
+                        temperature, work.data_ptr(), nbytes)
+    _launch("amk_verify_draft", _lib.amk_verify_draft, args, dev, stream,
+            (target_logits, draft_tokens, u, draft_logits, tokens, n_accepted, work))
     return tokens, n_accepted
+
+
+def ops_timeouts() -> int:
+    """CTAs of the operators' kernels that gave up a wait on the current device
+    since the library was loaded (amk_ops_timeouts): 0 on a sound device."""
+    n = abi.c_u32(0)
+    _check(abi.lib().amk_ops_timeouts(ctypes.byref(n)), "amk_ops_timeouts")
+    return n.value

@@ -491,3 +491,8 @@ def test_operators_on_another_stream_and_in_a_graph():
         torch.cuda.synchronize()
         for _, outs in graphs:
             assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_no_operator_gave_up_a_wait():
+    torch.cuda.synchronize()
+    assert amk.ops_timeouts() == 0
