@@ -87,7 +87,7 @@ typedef struct {
  * scales [out][ceil(in / 128)], w_jk = scale_j,k/128 * q_jk; every in must be
  * a multiple of 32.  amk_create packs each int4 matrix once into a copy the
  * handle owns (codes and scales of a row together); the caller's arrays are
- * not read by decode steps.  Scale arrays are ignored for bf16. */
+ * read by amk_extend, not by decode steps.  Scale arrays are ignored for bf16. */
 typedef struct {
     const void *embed;         /* bf16 [vocab][hidden] */
     const void *final_norm;    /* bf16 [hidden] */
@@ -311,6 +311,26 @@ AMK_API int amk_decode_step(amk_handle *h, int32_t token_id, int32_t pos,
  * Always synchronises the stream. */
 AMK_API int amk_decode_step_host(amk_handle *h, int32_t token_id, int32_t pos,
                          float *logits_host, int32_t *argmax_host);
+
+/* The multi-token step: n tokens at positions pos .. pos + n - 1 through the
+ * model in one call, as n calls of amk_decode_step would run them one by one
+ * (a prompt; drafted tokens with the token before them).  The weights are read
+ * once for all of the call's tokens (1024 at a time).  Appends K and V at the
+ * tokens' rows, attends over the rows up to each token's own, and writes the
+ * logits of the last n_logits tokens (0 .. n) to logits_dev, fp32
+ * [n_logits][vocab].  Rows < pos must hold earlier values, as for a step.
+ * (No counterpart in the AutoMegaKernel pages.)
+ *  tokens: host int32 [n], read before the call returns.
+ * By matrix products over several tokens (amk_linear, amk_attention below), not
+ * the persistent kernel: their inputs are rounded to bf16 (the single-token
+ * step's to 15 bits or none), so logits differ from a step's by about 2^-9 of
+ * their size.  Asynchronous on the handle's stream, which must not be capturing
+ * (AMK_ERR_UNSUPPORTED).  The first call allocates the activations.  A step
+ * that follows with token_id -1 is refused (this call chooses no token: see
+ * amk_verify_draft, which does with n_draft 0).  With W4A16 weights the
+ * caller's arrays are read. */
+AMK_API int amk_extend(amk_handle *h, const int32_t *tokens, int32_t n, int32_t pos,
+               int32_t n_logits, float *logits_dev);
 
 /* Device pointers to layer's K and V cache blocks, each
  * bf16 [n_kv_heads][max_ctx][head_dim] (for synthetic long-context fills and

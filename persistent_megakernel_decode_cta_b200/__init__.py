@@ -7,6 +7,7 @@ There is no CPU fallback: without the built library every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Dict, List, Optional, Tuple
 
@@ -14,7 +15,7 @@ from . import abi
 
 __all__ = ["AmkError", "Decoder", "Plan", "validate_graph", "default_options", "version",
            "make_config", "weights_struct", "decode_step_noalloc", "read_ceiling",
-           "linear", "attention", "verify_draft", "ops_timeouts"]
+           "linear", "attention", "verify_draft", "ops_timeouts", "generate"]
 
 
 class AmkError(RuntimeError):
@@ -303,6 +304,34 @@ class Decoder:
         _check(rc, "amk_decode_step_host")
         return int(am.value)
 
+    def extend(self, tokens, pos: int, logits=None, n_logits: Optional[int] = None):
+        """The multi-token step (amk_extend): ``tokens`` (a sequence of ints) at
+        positions pos, pos + 1, ... in one call.  Returns the logits of the last
+        ``n_logits`` tokens (default: of ``logits``' rows, else 1), float32
+        [n_logits, vocab]: ``logits`` if given, else a new tensor."""
+        import torch
+        n, vocab = len(tokens), self.cfg.vocab
+        if n_logits is None:
+            n_logits = min(1, n) if logits is None else logits.shape[0]
+        # (ctypes would cut numbers off at 32 bits)
+        if not 0 <= n_logits <= n:
+            raise AmkError(abi.ERR["AMK_ERR_INVALID_ARG"], f"extend: {n_logits} logits of {n} tokens")
+        if not 0 <= pos <= self.cfg.max_ctx - n or any(not 0 <= t < vocab for t in tokens):
+            raise AmkError(abi.ERR["AMK_ERR_POS_RANGE"], f"extend: {n} tokens at {pos}: a position "
+                           f"outside [0, {self.cfg.max_ctx}) or a token outside [0, {vocab})")
+        toks = (abi.c_i32 * max(n, 1))(*tokens)
+        if logits is None:
+            with torch.cuda.stream(torch.cuda.ExternalStream(self.stream)) if self.stream else \
+                    contextlib.nullcontext():
+                logits = torch.empty((n_logits, vocab), dtype=torch.float32, device="cuda")
+        elif logits.dtype is not torch.float32 or logits.shape != (n_logits, vocab) or \
+                not logits.is_contiguous() or not logits.is_cuda:
+            raise AmkError(abi.ERR["AMK_ERR_INVALID_ARG"],
+                           f"logits is not a contiguous CUDA float32 [{n_logits}, vocab] tensor")
+        _check(abi.lib().amk_extend(self._h, toks, n, int(pos), int(n_logits),
+                                    logits.data_ptr()), "amk_extend")
+        return logits
+
     def reset(self):
         _check(abi.lib().amk_reset_kv(self._h), "amk_reset_kv")
 
@@ -382,3 +411,4 @@ class Decoder:
 
 
 from .ops import attention, linear, ops_timeouts, verify_draft  # noqa: E402  (they use AmkError and _check)
+from .speculative import generate  # noqa: E402

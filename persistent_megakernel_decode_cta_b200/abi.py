@@ -162,6 +162,7 @@ SIGNATURES = {
     "amk_reset_kv": (ctypes.c_int, [c_vp]),
     "amk_decode_step": (ctypes.c_int, [c_vp, c_i32, c_i32, c_vp, ctypes.POINTER(c_i32)]),
     "amk_decode_step_host": (ctypes.c_int, [c_vp, c_i32, c_i32, c_vp, ctypes.POINTER(c_i32)]),
+    "amk_extend": (ctypes.c_int, [c_vp, ctypes.POINTER(c_i32), c_i32, c_i32, c_i32, c_vp]),
     "amk_get_kv": (ctypes.c_int, [c_vp, c_i32, ctypes.POINTER(c_vp), ctypes.POINTER(c_vp)]),
     "amk_get_logits": (ctypes.c_int, [c_vp, ctypes.POINTER(c_vp)]),
     "amk_get_stats": (ctypes.c_int, [c_vp, ctypes.POINTER(PlanStats)]),

@@ -18,6 +18,7 @@
 #include <vector>
 
 #include "amk.h"
+#include "amk_extend.h"
 #include "amk_internal.h"
 #include "amk_plan.h"
 
@@ -192,6 +193,11 @@ struct amk_handle {
     unsigned long long *h_key = nullptr;   // pinned
     cudaEvent_t err_ev = nullptr;
     bool err_pending = false;
+    // the multi-token step: the caller's weights, and its activations (from the
+    // first amk_extend on)
+    amk::ModelWeights weights{};
+    amk::ExtendBuffers ext{};
+    bool extended = false;  // the last tokens came by amk_extend, not by a step
     KParams kp{};
     uint32_t epoch = 0;
     uint32_t arrive_base = 0;  // attention chunk arrivals so far, per (layer, kv head)
@@ -356,6 +362,7 @@ int zero_state(amk_handle *H)
     if (e != cudaSuccess)
         return cuda_fail(e, "amk_reset_kv");
     H->epoch = 0;
+    H->extended = false;
     H->epoch0 = 0;
     H->tag = 0;  // the flagged words were cleared with the block above
     H->arrive_base = 0;
@@ -578,6 +585,20 @@ extern "C" int amk_create(const amk_config *cfg, const amk_weights *w, const amk
         free_handle(H);
         return cuda_fail(e, "amk_create");
     }
+    amk::ModelWeights &mw = H->weights;
+    mw.embed = w->embed;
+    mw.final_norm = w->final_norm;
+    mw.lm_head = w->lm_head;
+    mw.lm_head_scale = w->lm_head_scale;
+    mw.norm[0].assign(w->attn_norm, w->attn_norm + L);
+    mw.norm[1].assign(w->ffn_norm, w->ffn_norm + L);
+    const void *const *wm[7] = {w->wq, w->wk, w->wv, w->wo, w->wgate, w->wup, w->wdown};
+    const void *const *ws[7] = {w->sq, w->sk, w->sv, w->so, w->sgate, w->sup, w->sdown};
+    for (int m = 0; m < 7; ++m) {
+        mw.mat[m].assign(wm[m], wm[m] + L);
+        if (qm != AMK_QUANT_BF16)
+            mw.scale[m].assign(ws[m], ws[m] + L);
+    }
     KParams &k = H->kp;
     k.tasks = H->d_tasks;
     k.queue_off = H->d_qoff;
@@ -672,7 +693,7 @@ int launch_step(amk_handle *H, int32_t token_id, int32_t pos, float *logits_dev,
         return amk_set_error(AMK_ERR_POS_RANGE, "pos %d outside [0, %d)", pos, c.max_ctx);
     if (token_id >= c.vocab || token_id < -1)
         return amk_set_error(AMK_ERR_POS_RANGE, "token %d outside [0, %d)", token_id, c.vocab);
-    if (token_id == -1 && H->epoch == 0)
+    if (token_id == -1 && (H->epoch == 0 || H->extended))
         return amk_set_error(AMK_ERR_INVALID_ARG, "token -1 needs a previous step");
     if (logits_dev && ((uintptr_t)logits_dev % 4))
         return amk_set_error(AMK_ERR_INVALID_ARG, "logits_dev misaligned");
@@ -719,6 +740,7 @@ int launch_step(amk_handle *H, int32_t token_id, int32_t pos, float *logits_dev,
                              "cooperative launch: %s", cudaGetErrorString(e));
     }
     H->epoch += 1;
+    H->extended = false;
     H->tag += 1;
     if (at0)
         H->epoch0 += 1;
@@ -788,6 +810,71 @@ extern "C" int amk_decode_step_host(amk_handle *h, int32_t token_id, int32_t pos
             return cuda_fail(e, "logits copy");
     }
     return finish_sync(h, argmax_host);
+}
+
+// Tokens that amk_extend runs at a time: enough for the products to be bound by
+// the tensor cores, few enough that the activations stay small beside the weights.
+constexpr int32_t kExtendChunk = 1024;
+
+extern "C" int amk_extend(amk_handle *h, const int32_t *tokens, int32_t n, int32_t pos,
+                          int32_t n_logits, float *logits_dev)
+{
+    auto bad = [](const char *what) {
+        return amk_set_error(AMK_ERR_INVALID_ARG, "amk_extend: %s", what);
+    };
+    if (!h)
+        return bad("NULL handle");
+    const amk_config &c = h->plan->cfg;
+    if (n < 0 || n_logits < 0 || n_logits > n)
+        return bad("n < 0, or n_logits outside [0, n]");
+    if ((n && !tokens) || (n_logits && !logits_dev))
+        return bad("tokens or logits_dev is NULL");
+    if ((uintptr_t)logits_dev % 4)
+        return bad("logits_dev misaligned");
+    int rc = poll_pending_error(h);
+    if (rc != AMK_OK)
+        return rc;
+    if (h->poisoned)
+        return amk_set_error(AMK_ERR_POISONED, "handle poisoned; call amk_reset_kv");
+    if (pos < 0 || (int64_t)pos + n > c.max_ctx)
+        return amk_set_error(AMK_ERR_POS_RANGE, "amk_extend: positions %d .. %lld outside [0, %d)",
+                             pos, (long long)pos + n - 1, c.max_ctx);
+    for (int32_t i = 0; i < n; ++i)
+        if (tokens[i] < 0 || tokens[i] >= c.vocab)
+            return amk_set_error(AMK_ERR_POS_RANGE, "amk_extend: token %d outside [0, %d)",
+                                 tokens[i], c.vocab);
+    if (n == 0)
+        return AMK_OK;
+    cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(h->stream, &capturing);
+    if (e != cudaSuccess)
+        return cuda_fail(e, "amk_extend");
+    if (capturing != cudaStreamCaptureStatusNone)
+        return amk_set_error(AMK_ERR_UNSUPPORTED, "amk_extend: the stream is capturing (the tokens "
+                             "are read from host memory by the call)");
+    if (!h->ext.chunk) {
+        const int32_t chunk = std::min(c.max_ctx, kExtendChunk);
+        void *block = nullptr;
+        if ((rc = dalloc(h, &block, amk::extend_bytes(c, chunk))) != AMK_OK)
+            return rc;
+        h->ext = amk::extend_buffers(c, chunk, block);
+    }
+    h->extended = true;
+    for (int32_t i = 0; i < n; i += h->ext.chunk) {
+        const int32_t m = std::min(h->ext.chunk, n - i);
+        // of this chunk's tokens, those among the last n_logits of the call
+        const int32_t first = std::max(i, n - n_logits), want = std::max(0, i + m - first);
+        e = cudaMemcpyAsync(h->ext.tokens, tokens + i, sizeof(int32_t) * (size_t)m,
+                            cudaMemcpyHostToDevice, h->stream);
+        if (e != cudaSuccess)
+            return cuda_fail(e, "amk_extend");
+        float *out = want ? logits_dev + (size_t)(first - (n - n_logits)) * c.vocab : nullptr;
+        rc = amk::extend_chunk(c, h->weights, h->ext, h->d_kv, m, pos + i, 0, 0, want, out,
+                               h->stream);
+        if (rc != AMK_OK)
+            return rc;
+    }
+    return AMK_OK;
 }
 
 extern "C" int amk_get_kv(amk_handle *h, int32_t layer, void **k_dev, void **v_dev)

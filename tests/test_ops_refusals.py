@@ -101,6 +101,13 @@ def test_null_arguments_and_empty_calls():
     assert attention(n_tokens=0) == abi.AMK_OK
 
 
+def test_extend_refuses():
+    lib = abi.lib()
+    assert lib.amk_extend(None, None, 0, 0, 0, None) == INVALID
+    assert "amk_extend" in lib.amk_last_error().decode()
+    assert lib.amk_ops_timeouts(None) == INVALID
+
+
 def test_good_calls_without_a_device():
     import torch
     if torch.cuda.is_available():
