@@ -166,6 +166,12 @@ typedef struct {
                                  down projection as 32-bit words: the fp32 value rounded to 15 mantissa bits (a
                                  relative error of at most 2^-16), an 8-bit tag in its
                                  low byte */
+    int32_t attn_window;      /* models with a sliding window: a token attends to the last
+                                 attn_window rows up to its own, and to the first attn_sinks
+                                 rows of the cache, in steps and amk_extend alike; 0
+                                 (default): to all rows.  Rows keep their positions, the
+                                 cache max_ctx of them */
+    int32_t attn_sinks;
 } amk_options;
 
 typedef struct amk_handle amk_handle;

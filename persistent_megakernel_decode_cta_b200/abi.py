@@ -50,7 +50,8 @@ class Options(ctypes.Structure):
                 ("debug_skip_signal_task", c_i32), ("profile", c_i32),
                 ("l2_prefetch_kb", c_i32), ("ffn_fused", c_i32),
                 ("pos0_plan", c_i32), ("inflight_kb", c_i32), ("copy_piece_kb", c_i32),
-                ("sm_rotate", c_i32), ("debug_checks", c_i32), ("flagged_waits", c_i32)]
+                ("sm_rotate", c_i32), ("debug_checks", c_i32), ("flagged_waits", c_i32),
+                ("attn_window", c_i32), ("attn_sinks", c_i32)]
 
 
 class GraphWait(ctypes.Structure):

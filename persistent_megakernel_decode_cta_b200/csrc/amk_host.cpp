@@ -700,7 +700,12 @@ int launch_step(amk_handle *H, int32_t token_id, int32_t pos, float *logits_dev,
     KParams k = H->kp;
     k.pos = pos;
     k.token = token_id;
-    k.att_chunk = amk::attn_chunk_len(pos + 1, H->plan->opt.attn_splits);
+    const amk::VisibleRows vis =
+        amk::visible_rows(pos, H->plan->opt.attn_window, H->plan->opt.attn_sinks);
+    k.att_n = vis.n;
+    k.att_sinks = vis.sinks;
+    k.att_gap = vis.gap;
+    k.att_chunk = amk::attn_chunk_len(vis.n, H->plan->opt.attn_splits);
     k.att_P = H->plan->opt.stage_bytes / (4 * c.head_dim);
     // counter epochs count the steps each schedule ran (parity counts all)
     k.epoch = H->epoch - H->epoch0;
@@ -745,7 +750,7 @@ int launch_step(amk_handle *H, int32_t token_id, int32_t pos, float *logits_dev,
     if (at0)
         H->epoch0 += 1;
     {  // non-empty attention chunks of this step: each arrives once unless alone
-        const int C = H->plan->opt.attn_splits, n = pos + 1;
+        const int C = H->plan->opt.attn_splits, n = vis.n;
         const int chunk = amk::attn_chunk_len(n, C), nne = (n + chunk - 1) / chunk;
         if (nne > 1)
             H->arrive_base += (uint32_t)nne;
@@ -869,7 +874,8 @@ extern "C" int amk_extend(amk_handle *h, const int32_t *tokens, int32_t n, int32
         if (e != cudaSuccess)
             return cuda_fail(e, "amk_extend");
         float *out = want ? logits_dev + (size_t)(first - (n - n_logits)) * c.vocab : nullptr;
-        rc = amk::extend_chunk(c, h->weights, h->ext, h->d_kv, m, pos + i, 0, 0, want, out,
+        rc = amk::extend_chunk(c, h->weights, h->ext, h->d_kv, m, pos + i,
+                               h->plan->opt.attn_window, h->plan->opt.attn_sinks, want, out,
                                h->stream);
         if (rc != AMK_OK)
             return rc;

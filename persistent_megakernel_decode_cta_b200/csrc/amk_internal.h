@@ -54,6 +54,18 @@ inline __host__ __device__ int attn_chunk_len(int n, int splits)
     const int c = (n + splits - 1) / splits;
     return c > kMinAttnChunk ? c : kMinAttnChunk;
 }
+// The cache rows that the token at pos sees, in order: the first `sinks` rows
+// and the last `window` up to pos (all without a window).  Row v of them is
+// cache row v for v < sinks, else v + gap.
+struct VisibleRows {
+    int32_t n, sinks, gap;
+};
+inline VisibleRows visible_rows(int pos, int window, int sinks)
+{
+    const int lo = window > 0 && pos >= window ? pos - window + 1 : 0;
+    const int s = sinks < lo ? sinks : lo;
+    return {pos + 1 - lo + s, s, lo - s};
+}
 constexpr int kMaxStages = 16;
 // A ring stage's copy goes out in up to kPieces pieces of about KParams::piece bytes,
 // each completing on its own mbarrier, so that the producer can keep a
@@ -174,6 +186,7 @@ struct KParams {
     uint32_t inflight;          // cap on bulk-copy bytes in flight per SM (0xffffffff: none)
     uint32_t piece;             // bytes of a copy piece (multiple of 16)
     int32_t att_chunk;          // positions per split-K attention chunk at this step
+    int32_t att_n, att_sinks, att_gap;  // this step's VisibleRows
     int32_t att_P;              // KV positions per ring stage (stage_bytes / (4 head_dim))
     int32_t skip_signal_task;   // test hook, -1 = off (with flagged waits: that task's
                                 // flagged words carry a wrong tag)

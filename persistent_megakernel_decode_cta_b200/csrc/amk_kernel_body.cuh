@@ -501,14 +501,14 @@ __device__ __forceinline__ Geom task_geom(const KParams &p, const TaskDesc &d)
     Geom g{};
     if (d.kind == TK_ATTN) {
         const int c = d.r1;
-        const int n = p.pos + 1;
-        const int chunk = p.att_chunk;  // positions per chunk at this step
+        const int n = p.att_n;          // visible cache rows, this step's last
+        const int chunk = p.att_chunk;  // of them per chunk at this step
         g.j0 = c * chunk;
         g.j1 = min(g.j0 + chunk, n);
         if (g.j1 < g.j0)
             g.j1 = g.j0;
         g.pa = g.j0;
-        g.pb = max(g.pa, min(g.j1, p.pos));
+        g.pb = max(g.pa, min(g.j1, n - 1));
         g.P = p.att_P;
         g.nchunks = (g.pb - g.pa + g.P - 1) / g.P;
         return g;
@@ -575,7 +575,7 @@ __device__ __forceinline__ void lookahead_load(const KParams &p, Lookahead &la)
     const uint8_t *w0 = reinterpret_cast<const uint8_t *>(w.x);
     const uint8_t *w1 = reinterpret_cast<const uint8_t *>(w.y);
     if (d.kind == TK_ATTN) {
-        const size_t o = (size_t)g.pa * p.head_dim * 2;
+        const size_t o = (size_t)(g.pa + (g.pa < p.att_sinks ? 0 : p.att_gap)) * p.head_dim * 2;
         la.a = w0 + o;
         la.b = w1 + o;
         la.na = la.nb = (uint32_t)(g.pb - g.pa) * p.head_dim * 2;
@@ -756,7 +756,10 @@ __device__ void producer_loop(const KParams &p, const SmemLayout &s, int qb, int
                 // K rows on piece 0, V rows on piece 1
                 const int a = g.pa + i * g.P;
                 const int b = min(a + g.P, g.pb);
-                const uint32_t nb = (uint32_t)(b - a) * p.head_dim * 2;
+                const uint32_t row = (uint32_t)p.head_dim * 2, nb = (uint32_t)(b - a) * row;
+                // visible row v is cache row v among the sinks, v + att_gap behind
+                // them: a range across that border takes two copies
+                const int na = min(max(p.att_sinks - a, 0), b - a);
                 for (int h = 0; h < 2 && !stop; ++h) {
                     if (!flight_reserve(p, s, fl, nb, done_below, prof_wait)) {
                         stop = true;
@@ -764,8 +767,13 @@ __device__ void producer_loop(const KParams &p, const SmemLayout &s, int qb, int
                     }
                     const uint32_t bar = bar0 + 8 * h;
                     mbar_arrive_expect_tx(bar, nb);
-                    bulk_g2s_nohint(dst + (uint32_t)h * g.P * p.head_dim * 2,
-                                    (h ? w1 : w0) + (size_t)a * p.head_dim * 2, nb, bar);
+                    const uint32_t to = dst + (uint32_t)h * g.P * row;
+                    const uint8_t *from = (h ? w1 : w0) + (size_t)a * row;
+                    if (na > 0)
+                        bulk_g2s_nohint(to, from, na * row, bar);
+                    if (na < b - a)
+                        bulk_g2s_nohint(to + na * row, from + (size_t)(na + p.att_gap) * row,
+                                        nb - na * row, bar);
                     flight_push(s, fl, bar, par, nb, k);
                     ++used;
                 }
@@ -2055,7 +2063,7 @@ __device__ __forceinline__ bool attn_chunk(const KParams &p, const SmemLayout &s
     consumer_bar();
     if (*reinterpret_cast<volatile int *>(s.flags))
         return false;
-    if (g.j0 <= p.pos && p.pos < g.j1 && warp == 0) {
+    if (g.j0 < p.att_n && p.att_n <= g.j1 && warp == 0) {
         // the new position: K and V rows of this step (bf16 values as
         // floats), taken by position group 0
         float sc = 0.f;
@@ -2113,7 +2121,7 @@ __device__ __forceinline__ bool attn_chunk(const KParams &p, const SmemLayout &s
     consumer_bar();
     // the only non-empty chunk of the step writes the normalised output of
     // its heads directly; otherwise the partial (m, l, o) for the merge
-    const bool direct = g.j0 == 0 && g.j1 == p.pos + 1;
+    const bool direct = g.j0 == 0 && g.j1 == p.att_n;
     float *out = p.part + ((((size_t)l * nkv + gi) * p.attn_splits + c) * G) * (hd + 2);
     uint64_t *fin = p.attn + (size_t)l * nh * hd + (size_t)gi * G * hd;
     for (int i = ct; i < G * hd; i += kConsumerThreads) {
@@ -2250,7 +2258,7 @@ __device__ __forceinline__ bool attn_task(const KParams &p, const SmemLayout &s,
     if (!attn_chunk<E>(p, s, d, g, kc, ct, warp, lane, wt, otag))
         return false;
     const int l = d.layer, gi = d.r0, C = p.attn_splits;
-    const int n = p.pos + 1;
+    const int n = p.att_n;
     const int chunk = p.att_chunk;
     const int nne = (n + chunk - 1) / chunk;  // non-empty chunks: 0 .. nne-1
     if (nne == 1 || g.j1 <= g.j0)

@@ -94,7 +94,11 @@ int amk_lower(const amk_config *cfg, const amk_options *opt_in, int n_sms, amk_p
         opt.debug_checks = opt_in->debug_checks;
         if (opt_in->flagged_waits != 0) opt.flagged_waits = opt_in->flagged_waits;
         opt.n_sms = opt_in->n_sms;
+        opt.attn_window = opt_in->attn_window;
+        opt.attn_sinks = opt_in->attn_sinks;
     }
+    if (opt.attn_window < 0 || opt.attn_sinks < 0)
+        return amk_set_error(AMK_ERR_INVALID_ARG, "lowering: attn_window or attn_sinks < 0");
     const amk_config &c = *cfg;
     const int h = c.hidden, L = c.n_layers, nh = c.n_heads, nkv = c.n_kv_heads;
     const int hd = c.head_dim, F = c.ffn, V = c.vocab;

@@ -360,7 +360,11 @@ extern "C" int amk_decode_step_noalloc(const amk_plan *plan, const amk_weights *
     k.generic = P.generic;
     k.pos = pos;
     k.token = token_id;
-    k.att_chunk = amk::attn_chunk_len(pos + 1, P.opt.attn_splits);
+    const amk::VisibleRows vis = amk::visible_rows(pos, P.opt.attn_window, P.opt.attn_sinks);
+    k.att_n = vis.n;
+    k.att_sinks = vis.sinks;
+    k.att_gap = vis.gap;
+    k.att_chunk = amk::attn_chunk_len(vis.n, P.opt.attn_splits);
     k.att_P = P.opt.stage_bytes / (4 * c.head_dim);
     k.epoch = 0;   // counters were cleared above
     k.arrive_base = 0;

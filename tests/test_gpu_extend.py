@@ -6,8 +6,10 @@ rotated q, attention and SwiGLU outputs) to bf16: 2^-9 / sqrt(3) rms of each
 element, so each of the 2 L sublayers' outputs is off by at most 3e-3 of its own
 norm (three roundings in a row, and a half for what the norms pass on), added
 up like independent errors with the final norm's: 3e-3 sqrt(2 L + 1) of the
-logits' norm.  The largest of the errors and the largest logit stand in the
-same ratio to their norms."""
+logits' norm.  A single logit's error is a sum of many independent roundings,
+so nearly normal: none of the some 1e6 that are looked at here is beyond six
+times the root mean square (2e-9 each).
+"""
 import math
 
 import numpy as np
@@ -34,8 +36,11 @@ def tol(cfg):
 def close(cfg, got, want, what):
     got = got.double().cpu().numpy()
     assert np.isfinite(got).all()
-    err = np.abs(got - want).max() / np.abs(want).max()
-    assert err <= tol(cfg), f"{what}: {err:.3g} of the largest logit, tolerance {tol(cfg):.3g}"
+    size = np.sqrt((want**2).mean())
+    rms, worst = np.sqrt(((got - want)**2).mean()) / size, np.abs(got - want).max() / size
+    assert rms <= tol(cfg) and worst <= 6 * tol(cfg), (
+        f"{what}: error {rms:.3g} rms, {worst:.3g} at most, of the logits' root mean square; "
+        f"tolerance {tol(cfg):.3g} and six times that")
 
 
 def pair(cfg, seed=0):
@@ -193,7 +198,7 @@ def test_greedy_generation_is_the_targets_own(n_draft, same):
                        temperature=0.0)
     for i, (a, b) in enumerate(zip(want, got)):
         if a != b:  # only where two logits are as near as the two paths are
-            assert margins[i] <= 2 * tol(cfg), f"token {i}: {b}, not {a}"
+            assert margins[i] <= 12 * tol(cfg), f"token {i}: {b}, not {a}"
             break
     assert len(got) == 20
     target.close()
@@ -240,3 +245,108 @@ def test_generation_on_a_stream_of_its_own():
         amk.generate(here, prompt, 3, draft=draft)
     for d in (target, draft, here):
         d.close()
+
+
+# ---- sliding window ------------------------------------------------------------------
+
+class WindowedModel:
+    """The decoder in 64-bit numpy over all tokens at once, with a window and
+    sinks (the oracle has none); shared by the single- and multi-token paths."""
+
+    def __init__(self, cfg, w, window, sinks):
+        self.cfg, self.window, self.sinks = cfg, window, sinks
+        f = lambda t: t.double().cpu().numpy()  # noqa: E731
+        self.w = {k: [f(t) for t in v] if isinstance(v, list) else f(v)
+                  for k, v in w.items() if v is not None}
+
+    def logits(self, toks):
+        c, w, n = self.cfg, self.w, len(toks)
+
+        def norm(x, g):
+            return x / np.sqrt((x * x).mean(-1, keepdims=True) + c.rms_eps) * g
+
+        half = c.head_dim // 2
+        ang = np.arange(n)[:, None] * c.rope_theta ** (-np.arange(half) / half)
+        cs, sn = np.cos(ang)[:, None], np.sin(ang)[:, None]
+
+        def rope(x):
+            a, b = x[..., :half], x[..., half:]
+            return np.concatenate((a * cs - b * sn, b * cs + a * sn), -1)
+
+        i, j = np.arange(n)[:, None], np.arange(n)
+        seen = (j <= i) & ((j > i - self.window) | (j < self.sinks))
+        bf = lambda x: torch.tensor(x).to(torch.bfloat16).double().numpy()  # noqa: E731
+        x = w["embed"][toks]
+        for l in range(c.n_layers):
+            h = norm(x, w["attn_norm"][l])
+            q = rope((h @ w["wq"][l].T).reshape(n, c.n_heads, c.head_dim))
+            k = bf(rope((h @ w["wk"][l].T).reshape(n, c.n_kv_heads, c.head_dim)))
+            v = bf((h @ w["wv"][l].T).reshape(n, c.n_kv_heads, c.head_dim))
+            g = c.n_heads // c.n_kv_heads
+            o = np.empty_like(q)
+            for a in range(c.n_heads):
+                s = q[:, a] @ k[:, a // g].T / math.sqrt(c.head_dim)
+                s = np.where(seen, s, -np.inf)
+                p = np.exp(s - s.max(1, keepdims=True))
+                o[:, a] = p / p.sum(1, keepdims=True) @ v[:, a // g]
+            x = x + o.reshape(n, -1) @ w["wo"][l].T
+            h = norm(x, w["ffn_norm"][l])
+            z = h @ w["wgate"][l].T
+            x = x + (z / (1 + np.exp(-z)) * (h @ w["wup"][l].T)) @ w["wdown"][l].T
+        head = w["embed"] if c.tied else w["lm_head"]
+        return norm(x, w["final_norm"]) @ head.T
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (5, 0), (5, 3), (16, 1), (40, 4), (7, 100),
+                                          (200, 2), (70, 33)])
+def test_window_and_sinks(window, sinks):
+    """Single- and multi-token steps of a handle with a window: against 64 bits,
+    a step to the bf16 step tolerance, across several attention chunks."""
+    cfg = TINY.with_(max_ctx=160)
+    w = si.make_model(cfg, device="cuda")
+    toks = si.make_prompt(cfg, 150)
+    want = WindowedModel(cfg, w, window, sinks).logits(toks)
+    lg = torch.empty(cfg.vocab, device="cuda")
+    for flagged in (1, -1):
+        dec = amk.Decoder(cfg, w, options=amk.default_options(
+            attn_window=window, attn_sinks=sinks, flagged_waits=flagged, debug_checks=1))
+        for p, t in enumerate(toks):
+            dec.step(t, p, logits=lg)
+            err = np.abs(lg.double().cpu().numpy() - want[p]).max() / np.abs(want[p]).max()
+            assert err <= 0.5 * 1e-2, f"step {p}: {err:.3g}"
+        dec.reset()
+        got = dec.extend(toks[:101], 0, n_logits=101)
+        for p in range(101):
+            close(cfg, got[p], want[p], f"extend {p}")
+        dec.step(toks[101], 101, logits=lg)
+        close(cfg, lg, want[101], "step 101 behind extend")
+        got = dec.extend(toks[102:], 102, n_logits=48)
+        for i in range(48):
+            close(cfg, got[i], want[102 + i], f"extend {102 + i}")
+        assert dec.check_guards() == 0
+        dec.close()
+
+
+def test_window_of_the_no_allocation_step():
+    cfg = TINY.with_(max_ctx=96)
+    w = si.make_model(cfg, device="cuda")
+    toks = si.make_prompt(cfg, 90)
+    want = WindowedModel(cfg, w, 11, 2).logits(toks)
+    plan = amk.Plan(cfg, torch.cuda.get_device_properties(0).multi_processor_count,
+                    amk.default_options(attn_window=11, attn_sinks=2))
+    ws, keep = amk.weights_struct(cfg, w)
+    kv = torch.zeros((cfg.n_layers, 2, cfg.n_kv_heads, cfg.max_ctx, cfg.head_dim),
+                     dtype=torch.bfloat16, device="cuda")
+    lg = torch.empty(cfg.vocab, device="cuda")
+    for p, t in enumerate(toks):
+        amk.decode_step_noalloc(plan, ws, kv, t, p, lg, want_argmax=True)
+        err = np.abs(lg.double().cpu().numpy() - want[p]).max() / np.abs(want[p]).max()
+        assert err <= 0.5 * 1e-2, f"step {p}: {err:.3g}"
+    plan.close()
+
+
+def test_window_refusals():
+    with pytest.raises(amk.AmkError):
+        amk.Plan(TINY, 148, amk.default_options(attn_window=-1))
+    with pytest.raises(amk.AmkError):
+        amk.Plan(TINY, 148, amk.default_options(attn_window=4, attn_sinks=-1))
