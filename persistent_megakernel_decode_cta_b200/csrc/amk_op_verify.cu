@@ -12,6 +12,7 @@
 // logits are read once (the drawn row's again, from L2).
 #include <math.h>
 
+#include "amk_ops.cuh"
 #include "amk_ops.h"
 
 namespace amk {
@@ -33,6 +34,7 @@ struct VerifyParams {
     int32_t *out, *n_acc;
     RowStat *stat;     // [rows][chunks]
     double *weight;    // [chunks]: of the drawn row
+    float *tok_logit;  // [rows]: the drafted token's, where it is in the vocabulary
     uint32_t *done;    // CTAs of the second launch that have finished
     int64_t ts, ds;
     int32_t d, vocab, chunks, greedy;
@@ -44,24 +46,39 @@ __device__ __forceinline__ const float *row_ptr(const VerifyParams &p, int r)
     return r <= p.d ? p.target + r * p.ts : p.draft + (r - p.d - 1) * p.ds;
 }
 
-// exp((x - m) / temperature); 0 for a chunk or row without a finite logit
-__device__ __forceinline__ double weight_of(float x, float m, double inv_t)
+// exp(y) for y <= 0: y = (n / 64) ln 2 + r with |r| <= ln 2 / 128, so that
+// exp(y) = 2^(n >> 6) 2^((n & 63) / 64) exp(r), the second from a table and the
+// last by its series up to r^5 (the next term is below 2^-54).  ln 2 / 64 in
+// two parts keeps r exact.  Half the operations of a general exp.
+struct ExpTable {
+    double t[64];  // 2^(j / 64)
+};
+__device__ __forceinline__ void fill_table(ExpTable &e)
 {
-    return m == -INFINITY ? 0.0 : exp(((double)x - (double)m) * inv_t);
+    if (threadIdx.x < 64)
+        e.t[threadIdx.x] = exp2(threadIdx.x / 64.0);
 }
-
-__device__ __forceinline__ RowStat merge(const RowStat &a, const RowStat &b, double inv_t)
+__device__ __forceinline__ double exp_neg(const ExpTable &e, double y)
 {
-    RowStat r;
-    r.m = fmaxf(a.m, b.m);
-    // no FMA: the same sum for either order of a and b
-    r.sum = __dadd_rn(__dmul_rn(a.sum, weight_of(a.m, r.m, inv_t)),
-                      __dmul_rn(b.sum, weight_of(b.m, r.m, inv_t)));
-    r.arg = a.arg < 0 || b.arg < 0 ? -1
-            : a.m > b.m            ? a.arg
-            : b.m > a.m            ? b.arg
-                                   : min(a.arg, b.arg);
-    return r;
+    if (!(y > -700.0))  // below 1e-304: 0 beside the row's largest, which is 1; NaN stays
+        return y != y ? y : 0.0;
+    constexpr double kHi = 0x1.62e42fefa0000p-7, kLo = 0x1.cf79abc9e3b3ap-46;  // ln 2 / 64
+    const double s = fma(y, 92.332482616893656877, 6755399441055744.0);  // rounds to an integer
+    const int n = __double2loint(s);
+    const double f = s - 6755399441055744.0;
+    const double r = fma(f, -kLo, fma(f, -kHi, y));
+    double q = fma(r, 1.0 / 120, 1.0 / 24);
+    q = fma(r, q, 1.0 / 6);
+    q = fma(r, q, 0.5);
+    q = fma(r, q, 1.0);
+    const double t = e.t[n & 63];
+    const double v = fma(t * r, q, t);
+    return __hiloint2double(__double2hiint(v) + ((n >> 6) << 20), __double2loint(v));
+}
+// exp((x - m) / temperature); 0 for a chunk or row without a finite logit
+__device__ __forceinline__ double weight_of(const ExpTable &e, float x, float m, double inv_t)
+{
+    return m == -INFINITY ? 0.0 : exp_neg(e, ((double)x - (double)m) * inv_t);
 }
 
 // Sum over the CTA in a fixed order; every thread returns it.
@@ -103,12 +120,22 @@ __global__ void __launch_bounds__(kThreadsV) verify_stats(const VerifyParams p)
     __shared__ float wm[kWarps];
     __shared__ int wbad[kWarps], warg[kWarps];
     __shared__ double buf[kWarps];
+    __shared__ ExpTable et;
     const int c = blockIdx.x, r = blockIdx.y, tid = threadIdx.x;
+    fill_table(et);
+    ops::pdl_wait();
+    ops::pdl_launch();
     if (c == 0 && r == 0 && tid == 0)
         *p.done = 0;
     const int b = c * kChunk, e = min(b + kChunk, p.vocab);
+    const float *row = row_ptr(p, r);
     float x[kPer];
-    load_chunk(row_ptr(p, r), b, e, x);
+    load_chunk(row, b, e, x);
+    // the drafted token's logit in this row, for the second launch
+    const int i = r <= p.d ? r : r - p.d - 1;
+    const int drafted = tid == 0 && i < p.d ? __ldg(p.tok + i) : -1;
+    const bool here = drafted >= b && drafted < e;
+    const float its = here ? __ldg(row + drafted) : 0.f;
     float m = -INFINITY;
     int bad = 0;
 #pragma unroll
@@ -139,7 +166,7 @@ __global__ void __launch_bounds__(kThreadsV) verify_stats(const VerifyParams p)
     if (!p.greedy)
 #pragma unroll
         for (int j = 0; j < kPer; ++j)
-            s += weight_of(x[j], m, p.inv_t);
+            s += weight_of(et, x[j], m, p.inv_t);
     arg = __reduce_min_sync(0xffffffffu, arg);
     if ((tid & 31) == 0)
         warg[tid >> 5] = arg;
@@ -151,11 +178,14 @@ __global__ void __launch_bounds__(kThreadsV) verify_stats(const VerifyParams p)
         o.sum = s;
         o.m = m;
         o.arg = bad ? -1 : arg;
+        if (here)
+            p.tok_logit[r] = its;
         p.stat[(int64_t)r * p.chunks + c] = o;
     }
 }
 
 struct Shared {
+    ExpTable et;
     RowStat row[kMaxRows];
     double buf[kWarps];
     int n, stop, last_cta, pick, found, fallback;
@@ -172,15 +202,15 @@ struct Draw {
 
 // The weights of the thread's tokens of a chunk: max(p - q, 0), or, with
 // `whole`, p itself; returns their sum.
-__device__ double chunk_weights(const VerifyParams &p, const Draw &dr, int b, bool whole,
-                                double (&w)[kPer])
+__device__ double chunk_weights(const VerifyParams &p, const ExpTable &et, const Draw &dr, int b,
+                                bool whole, double (&w)[kPer])
 {
     const int e = min(b + kChunk, p.vocab);
     float x[kPer];
     load_chunk(dr.prow, b, e, x);
 #pragma unroll
     for (int j = 0; j < kPer; ++j)
-        w[j] = weight_of(x[j], dr.pm, p.inv_t);
+        w[j] = weight_of(et, x[j], dr.pm, p.inv_t);
     if (!whole) {
         if (dr.qrow) {
             load_chunk(dr.qrow, b, e, x);
@@ -188,7 +218,7 @@ __device__ double chunk_weights(const VerifyParams &p, const Draw &dr, int b, bo
             for (int j = 0; j < kPer; ++j)
                 // both products rounded (no FMA), so that equal rows leave exactly 0
                 w[j] = fmax(__dmul_rn(w[j], dr.fp) -
-                                __dmul_rn(weight_of(x[j], dr.qm, p.inv_t), dr.fq),
+                                __dmul_rn(weight_of(et, x[j], dr.qm, p.inv_t), dr.fq),
                             0.0);
         }
         const int at = dr.skip - (b + (int)threadIdx.x * kPer);
@@ -209,25 +239,49 @@ __global__ void __launch_bounds__(kThreadsV) verify_draw(const VerifyParams p)
     __shared__ Shared sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int R = p.d + 1 + (p.draft ? p.d : 0);
+    fill_table(sh.et);
     if (tid == 0)
         sh.n = p.d;
-    // the rows' statistics, merged in a fixed order
+    __syncthreads();
+    ops::pdl_wait();
+    ops::pdl_launch();
+    // the rows' statistics, merged in a fixed order: the largest logit first, so
+    // that a chunk's sum takes one exponential
+    const RowStat none = {0.0, -INFINITY, INT32_MAX};
+    auto stat_of = [&](int r) {  // the lane's chunk of the first 32
+        return r < R && lane < p.chunks ? p.stat[(int64_t)r * p.chunks + lane] : none;
+    };
+    RowStat next = stat_of(warp);
     for (int r = warp; r < R; r += kWarps) {
-        const RowStat *st = p.stat + (int64_t)r * p.chunks;
-        RowStat s = {0.0, -INFINITY, INT32_MAX};
-        for (int c = lane; c < p.chunks; c += 32)
-            s = merge(s, st[c], p.inv_t);
-#pragma unroll
-        for (int off = 16; off; off >>= 1) {
-            RowStat o;
-            o.sum = __shfl_xor_sync(0xffffffffu, s.sum, off);
-            o.m = __shfl_xor_sync(0xffffffffu, s.m, off);
-            o.arg = __shfl_xor_sync(0xffffffffu, s.arg, off);
-            s = merge(s, o, p.inv_t);
+        const RowStat *st = p.stat + (int64_t)r * p.chunks, s0 = next;
+        next = stat_of(r + kWarps);  // on its way while this row is merged
+        float m = s0.m;
+        int bad = s0.arg < 0;
+        for (int c = lane + 32; c < p.chunks; c += 32) {
+            m = fmaxf(m, st[c].m);
+            bad |= st[c].arg < 0;
         }
+#pragma unroll
+        for (int off = 16; off; off >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        bad = __any_sync(0xffffffffu, bad || m == -INFINITY);  // nothing but -inf: no distribution
+        double sum = s0.sum * weight_of(sh.et, s0.m, m, p.inv_t);
+        int arg = s0.m == m ? s0.arg : INT32_MAX;
+        for (int c = lane + 32; c < p.chunks; c += 32) {
+            const RowStat s = st[c];
+            sum += s.sum * weight_of(sh.et, s.m, m, p.inv_t);
+            if (s.m == m)
+                arg = min(arg, s.arg);
+        }
+        arg = __reduce_min_sync(0xffffffffu, arg);
+#pragma unroll
+        for (int off = 16; off; off >>= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, off);
         if (lane == 0) {
-            if (s.m == -INFINITY)
-                s.arg = -1;  // nothing but -inf
+            RowStat s;
+            s.sum = sum;
+            s.m = m;
+            s.arg = bad ? -1 : arg;
             sh.row[r] = s;
         }
     }
@@ -251,11 +305,11 @@ __global__ void __launch_bounds__(kThreadsV) verify_draw(const VerifyParams p)
                     const RowStat qs = sh.row[p.d + 1 + tid];
                     bad = bad || qs.arg < 0;
                     if (in)
-                        qt = weight_of(row_ptr(p, p.d + 1 + tid)[t], qs.m, p.inv_t) / qs.sum;
+                        qt = weight_of(sh.et, p.tok_logit[p.d + 1 + tid], qs.m, p.inv_t) / qs.sum;
                 }
                 if (in)
                     ok = (double)p.u[tid] * qt <
-                         weight_of(row_ptr(p, tid)[t], ps.m, p.inv_t) / ps.sum;
+                         weight_of(sh.et, p.tok_logit[tid], ps.m, p.inv_t) / ps.sum;
             }
         }
         if (bad || !ok)
@@ -293,17 +347,21 @@ __global__ void __launch_bounds__(kThreadsV) verify_draw(const VerifyParams p)
         dr.fq = 1.0 / sh.row[p.d + 1 + n].sum;
     }
     double w[kPer];
-    for (int c = blockIdx.x; c < p.chunks; c += gridDim.x) {
-        const double s = block_sum(chunk_weights(p, dr, c * kChunk, false, w), sh.buf);
+    double own = chunk_weights(p, sh.et, dr, blockIdx.x * kChunk, false, w);  // a CTA to a chunk
+    {
+        const double s = block_sum(own, sh.buf);
         if (tid == 0)
-            p.weight[c] = s;
+            p.weight[blockIdx.x] = s;
     }
     // the last CTA to finish draws: its counter update follows its own weights
     // and precedes its loads of the others'
     if (tid == 0) {
-        __threadfence();
-        sh.last_cta = atomicAdd(p.done, 1u) == gridDim.x - 1;
-        __threadfence();
+        sh.last_cta = 1;
+        if (gridDim.x > 1) {
+            __threadfence();
+            sh.last_cta = atomicAdd(p.done, 1u) == gridDim.x - 1;
+            __threadfence();
+        }
     }
     __syncthreads();
     if (!sh.last_cta)
@@ -313,7 +371,7 @@ __global__ void __launch_bounds__(kThreadsV) verify_draw(const VerifyParams p)
         // whole: max(p - q, 0) is 0 everywhere, p itself is drawn from
         if (whole) {
             for (int c = 0; c < p.chunks; ++c) {
-                const double s = block_sum(chunk_weights(p, dr, c * kChunk, true, w), sh.buf);
+                const double s = block_sum(chunk_weights(p, sh.et, dr, c * kChunk, true, w), sh.buf);
                 if (tid == 0)
                     p.weight[c] = s;
             }
@@ -364,7 +422,8 @@ __global__ void __launch_bounds__(kThreadsV) verify_draw(const VerifyParams p)
         if (sh.pick < 0)
             continue;  // the same for every thread
         const double x = sh.before;
-        const double own = chunk_weights(p, dr, sh.pick * kChunk, whole, w);
+        if (whole || sh.pick != (int)blockIdx.x)  // else the weights are still here
+            own = chunk_weights(p, sh.et, dr, sh.pick * kChunk, whole, w);
         double inc = own;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -404,8 +463,9 @@ __global__ void __launch_bounds__(kThreadsV) verify_draw(const VerifyParams p)
 int64_t workspace_bytes(int n_draft, int vocab)
 {
     const int64_t chunks = ((int64_t)vocab + kChunk - 1) / kChunk;
-    return (2 * (int64_t)n_draft + 1) * chunks * (int64_t)sizeof(RowStat) +
-           chunks * (int64_t)sizeof(double) + 16;
+    const int64_t rows = 2 * (int64_t)n_draft + 1;
+    return rows * chunks * (int64_t)sizeof(RowStat) + chunks * (int64_t)sizeof(double) +
+           rows * (int64_t)sizeof(float) + 16;
 }
 
 int check_verify(const amk_verify_args *a)
@@ -470,13 +530,21 @@ extern "C" int amk_verify_draft(const amk_verify_args *a, void *cuda_stream)
     const int rows = p.d + 1 + (p.draft ? p.d : 0);
     p.stat = static_cast<RowStat *>(a->workspace);
     p.weight = reinterpret_cast<double *>(p.stat + (int64_t)rows * p.chunks);
-    p.done = reinterpret_cast<uint32_t *>(p.weight + p.chunks);
-    cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-    verify_stats<<<dim3((unsigned)p.chunks, (unsigned)rows), kThreadsV, 0, st>>>(p);
-    cudaError_t e = cudaGetLastError();
+    p.tok_logit = reinterpret_cast<float *>(p.weight + p.chunks);
+    p.done = reinterpret_cast<uint32_t *>(p.tok_logit + rows);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)p.chunks, (unsigned)rows);
+    cfg.blockDim = dim3(kThreadsV);
+    cfg.stream = static_cast<cudaStream_t>(cuda_stream);
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, verify_stats, p);
     if (e == cudaSuccess) {
-        verify_draw<<<(unsigned)p.chunks, kThreadsV, 0, st>>>(p);
-        e = cudaGetLastError();
+        cfg.gridDim = dim3((unsigned)p.chunks);
+        e = cudaLaunchKernelEx(&cfg, verify_draw, p);
     }
     return launch_status(e, "amk_verify_draft");
 }

@@ -19,6 +19,7 @@ _INVALID = abi.ERR["AMK_ERR_INVALID_ARG"]
 _pack_linear = abi.packer(abi.LinearArgs)
 _pack_attention = abi.packer(abi.AttentionArgs)
 _pack_verify = abi.packer(abi.VerifyArgs)
+_workspace = {}  # bytes by (drafts, vocab)
 _torch = None
 _lib = _raw_stream = _device = None
 
@@ -89,7 +90,7 @@ def _new(like, stream, shape, dtype):
     """A result on the device of `like`, from the pool of the stream that will
     write it."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return like.new_empty(shape) if like.dtype is dtype else like.new_empty(shape, dtype=dtype)
     side = _torch.cuda.ExternalStream(stream, device=like.device)
     with _torch.cuda.stream(side):
         return like.new_empty(shape, dtype=dtype)
@@ -231,7 +232,7 @@ def attention(q, k, v, pos: int, *, window: int = 0, sinks: int = 0,
     T, nh, hd = qs
     nkv, rows, _ = ks
     if out is None:
-        out = _new(q, stream, qs, bf16)
+        out = _torch.empty_like(q) if stream is None else _new(q, stream, qs, bf16)
     elif out.dtype is not bf16 or out.shape != qs:
         _refuse("attention: out must be bfloat16 of q's shape")
     (qt, qh, q1), (kh, kr, k1), (vh, vr, v1), (ot, oh, o1) = (q.stride(), k.stride(), v.stride(),
@@ -280,9 +281,14 @@ def verify_draft(target_logits, draft_tokens, u, *, draft_logits=None, temperatu
     d, vocab = ts[0] - 1, ts[1]
     if vocab > _I32 or d > _I32:
         _refuse("verify_draft: a size above 2^31 - 1")
-    nbytes = _lib.amk_verify_workspace(d, vocab)
-    if nbytes < 0:
-        _check(int(nbytes), "amk_verify_workspace")
+    nbytes = _workspace.get((d, vocab))
+    if nbytes is None:
+        nbytes = _lib.amk_verify_workspace(d, vocab)
+        if nbytes < 0:
+            _check(int(nbytes), "amk_verify_workspace")
+        if len(_workspace) >= 256:
+            _workspace.clear()
+        _workspace[d, vocab] = nbytes
     if draft_tokens.dtype is not i32 or draft_tokens.shape != (d,) or \
             not draft_tokens.is_contiguous():
         _refuse(f"verify_draft: draft_tokens is not contiguous int32 [{d}]")
@@ -298,14 +304,14 @@ def verify_draft(target_logits, draft_tokens, u, *, draft_logits=None, temperatu
             _refuse(f"verify_draft: draft_logits is not float32 [{d}, {vocab}] with contiguous rows")
         dstr, dp = draft_logits.stride(0), draft_logits.data_ptr()
     if tokens is None:
-        tokens = _new(u, stream, (d + 1,), i32)
+        tokens = _new(draft_tokens, stream, (d + 1,), i32)
     elif tokens.dtype is not i32 or tokens.shape != (d + 1,) or not tokens.is_contiguous():
         _refuse(f"verify_draft: tokens is not contiguous int32 [{d + 1}]")
     if n_accepted is None:
-        n_accepted = _new(u, stream, (1,), i32)
+        n_accepted = _new(draft_tokens, stream, (1,), i32)
     elif n_accepted.dtype is not i32 or n_accepted.shape != (1,):
         _refuse("verify_draft: n_accepted is not int32 [1]")
-    work = _new(u, stream, (nbytes,), torch.uint8)
+    work = _new(draft_tokens, stream, ((nbytes + 3) >> 2,), i32)
     args = _pack_verify(target_logits.data_ptr(), dp, u.data_ptr(), draft_tokens.data_ptr(),
                         tokens.data_ptr(), n_accepted.data_ptr(), tstr, dstr, d, vocab,
                         temperature, work.data_ptr(), nbytes)
