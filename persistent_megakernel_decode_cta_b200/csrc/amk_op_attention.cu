@@ -508,10 +508,352 @@ cudaError_t launch_tiles(TileParams &p, cudaStream_t stream)
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// ---- long prompts: tcgen05 --------------------------------------------------------
+// Tiles of 128 rows (as above), one CTA each, two CTAs to an SM so that one's
+// products run under the other's softmax.  Both products run on tcgen05: S = Q
+// K^T into one of two TMEM buffers, O += P V into a third, with P through
+// shared memory in the layout the MMA reads, and V taken as it lies in the
+// cache (its rows are the K of that product).  A thread of the four softmax
+// warps has a row to itself: maximum and sum need no shuffles.  O is rescaled
+// only when a row's maximum has grown by more than 8 (a factor of 256, exact
+// in fp32 and bf16 alike); until then the weights are taken against the
+// earlier maximum, which the final division by their sum makes good.
+template <int HD>
+struct TcCfg {
+    static constexpr int SUB = HD / 64;               // blocks of 64 elements of a head
+    static constexpr int Q = SUB * 128 * 128, KV = SUB * kKeys * 128, P = 128 * 128;
+    static constexpr int BARS = Q + 4 * KV + P;       // two stages of K and of V
+    static constexpr int SMEM = BARS + 256;
+    static constexpr int THREADS = 256, COLS = 256;   // TMEM: two S of 64 columns, O from 128 on
+};
+
+template <int HD>
+__global__ void __launch_bounds__(TcCfg<HD>::THREADS, 2)
+    attn_tc(const __grid_constant__ TileParams p)
+{
+    using C = TcCfg<HD>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t base = smem_u32(smem);
+    const uint32_t qs = base, ks = qs + C::Q, vs = ks + 2 * C::KV, ps = vs + 2 * C::KV;
+    const uint32_t bar0 = base + C::BARS;
+    const uint32_t q_full = bar0, p_full = bar0 + 8, o_done = bar0 + 16;
+    auto k_full = [&](int b) { return bar0 + 24 + 8 * b; };
+    auto k_empty = [&](int b) { return bar0 + 40 + 8 * b; };
+    auto v_full = [&](int b) { return bar0 + 56 + 8 * b; };
+    auto v_empty = [&](int b) { return bar0 + 72 + 8 * b; };
+    auto s_full = [&](int b) { return bar0 + 88 + 8 * b; };
+    auto s_free = [&](int b) { return bar0 + 104 + 8 * b; };
+    int *flags = reinterpret_cast<int *>(smem + C::BARS + 128);  // TMEM address, failure
+    volatile int *fail = flags + 1;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        flags[1] = (base & 1023) != 0;  // the swizzled layouts count from 1024-byte boundaries
+        mbar_init(q_full, 4);
+        mbar_init(p_full, 4);
+        mbar_init(o_done, 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(k_full(b), 1);
+            mbar_init(k_empty(b), 1);
+            mbar_init(v_full(b), 1);
+            mbar_init(v_empty(b), 1);
+            mbar_init(s_full(b), 1);
+            mbar_init(s_free(b), 4);
+        }
+        mbar_init_fence();
+        prefetch_map(&p.k);
+        prefetch_map(&p.v);
+    }
+    if (warp == 2)
+        tmem_alloc<C::COLS>(smem_u32(flags));
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(flags);
+    const AttnParams &a = p.a;
+    const int kvh = blockIdx.x % p.n_kv;
+    const int r0 = (p.tiles - 1 - blockIdx.x / p.n_kv) * 128;  // the longest rows start first
+    const int nrows = min(128, p.rows - r0);
+    const int pmin = a.pos + r0 / a.group, pmax = a.pos + (r0 + nrows - 1) / a.group;
+    int na, lo;
+    visible(a, pmin, na, lo);
+    const int ta = (na + kKeys - 1) / kKeys, tn = *fail ? 0 : ta + (pmax - lo + kKeys) / kKeys;
+    auto first_key = [&](int i) { return i < ta ? i * kKeys : lo + (i - ta) * kKeys; };
+    pdl_wait();
+    pdl_launch();
+    if (warp == 0) {
+        bool ok = true;
+        int i = 0;
+        for (; i < tn; ++i) {
+            const int b = i & 1;
+            const uint32_t ph = ((i >> 1) & 1) ^ 1;
+            if (!warp_wait(k_empty(b), ph, fail)) {
+                ok = false;
+                break;
+            }
+            if (elect_one()) {
+                mbar_expect_tx(k_full(b), C::KV);
+#pragma unroll
+                for (int d = 0; d < C::SUB; ++d)
+                    tma_3d(ks + b * C::KV + d * kKeys * 128, &p.k, d * 64, first_key(i), kvh,
+                           k_full(b));
+            }
+            __syncwarp();
+            if (!warp_wait(v_empty(b), ph, fail)) {
+                // K's copy of this stage is on its way
+                for (int n = 0; n < (1 << 20) && !mbar_try_wait(k_full(b), ph ^ 1); ++n) {
+                }
+                ok = false;
+                break;
+            }
+            if (elect_one()) {
+                mbar_expect_tx(v_full(b), C::KV);
+#pragma unroll
+                for (int d = 0; d < C::SUB; ++d)
+                    tma_3d(vs + b * C::KV + d * kKeys * 128, &p.v, d * 64, first_key(i), kvh,
+                           v_full(b));
+            }
+            __syncwarp();
+        }
+        if (!ok)  // no copy may land after the CTA has gone
+            for (int j = max(0, i - 2); j < i; ++j)
+                for (int n = 0; n < (1 << 20) && !(mbar_try_wait(k_full(j & 1), (j >> 1) & 1) &&
+                                                   mbar_try_wait(v_full(j & 1), (j >> 1) & 1));
+                     ++n) {
+                }
+    } else if (warp == 1) {
+        constexpr uint32_t is = tc_idesc(128, kKeys), io = tc_idesc(128, HD, true);
+        auto pv = [&](int j) {  // O += P V of keys j
+            const int b = j & 1;
+            if (!warp_wait(p_full, j & 1, fail) || !warp_wait(v_full(b), (j >> 1) & 1, fail))
+                return false;
+            tc_fence_after();
+            const uint64_t pd = tc_desc(ps), vd = tc_desc_mn(vs + b * C::KV, kKeys * 128);
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < kKeys / 16; ++k)  // 16 keys: 32 bytes of P, 16 rows of V
+                    tc_mma(tmem + 128, pd + 2 * k, vd + k * (16 * 128 >> 4), io, j + k ? 1u : 0u);
+                tc_commit(v_empty(b));
+                tc_commit(o_done);
+            }
+            __syncwarp();
+            return true;
+        };
+        bool ok = tn == 0 || warp_wait(q_full, 0, fail);
+        for (int i = 0; i < tn && ok; ++i) {
+            const int b = i & 1;
+            if (!warp_wait(k_full(b), (i >> 1) & 1, fail) ||
+                !warp_wait(s_free(b), ((i >> 1) & 1) ^ 1, fail)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint64_t qd = tc_desc(qs), kd = tc_desc(ks + b * C::KV);
+            if (elect_one()) {
+#pragma unroll
+                for (int d = 0; d < C::SUB; ++d)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tc_mma(tmem + b * kKeys, qd + d * (128 * 128 >> 4) + 2 * k,
+                               kd + d * (kKeys * 128 >> 4) + 2 * k, is, d + k ? 1u : 0u);
+                tc_commit(k_empty(b));
+                tc_commit(s_full(b));
+            }
+            __syncwarp();
+            if (i > 0)
+                ok = pv(i - 1);
+        }
+        if (ok && tn > 0)
+            pv(tn - 1);
+    } else if (warp >= 4) {
+        const int r = tid - 128, row = r0 + r;
+        const bool in = r < nrows;
+        const int tok = in ? row / a.group : 0, h = kvh * a.group + (in ? row % a.group : 0);
+        const int pr = in ? a.pos + tok : pmax;
+        {  // the row's query, into the layout the MMA reads
+            const uint16_t *q = a.q + tok * a.q_ts + h * a.q_hs;
+#pragma unroll
+            for (int c = 0; c < HD / 8; ++c) {
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (in && c * 8 + 8 <= a.hd) {
+                    x = __ldg(reinterpret_cast<const uint4 *>(q) + c);
+                } else if (in && c * 8 < a.hd) {
+                    uint16_t e[8] = {};
+                    for (int j = 0; c * 8 + j < a.hd; ++j)
+                        e[j] = q[c * 8 + j];
+                    memcpy(&x, e, 16);
+                }
+                sts128(qs + (c >> 3) * 128 * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4), x.x, x.y,
+                       x.z, x.w);
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(q_full);
+        }
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int i = 0; i < tn; ++i) {
+            const int b = i & 1, j0 = first_key(i);
+            if (!warp_wait(s_full(b), (i >> 1) & 1, fail)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            float s[kKeys];
+#pragma unroll
+            for (int c = 0; c < kKeys; c += 16)
+                tmem_ld16(tmem + lanes + b * kKeys + c, *reinterpret_cast<float(*)[16]>(s + c));
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(s_free(b));
+            const bool sink = i < ta;
+            if (sink ? j0 + kKeys > na
+                     : j0 + kKeys - 1 > pmin || (a.window && j0 <= pmax - a.window)) {
+                // keys j0 + e of the row: e < hi, and e >= from or e < sinks
+                const int hi = sink ? na - j0 : pr - j0 + 1;
+                const int from = !sink && a.window ? pr - a.window + 1 - j0 : 0;
+                const int sk = sink ? 0 : a.sinks - j0;
+#pragma unroll
+                for (int e = 0; e < kKeys; ++e)
+                    if (!(e < hi && (e >= from || e < sk)))
+                        s[e] = -INFINITY;
+            }
+            float mx = s[0];
+#pragma unroll
+            for (int e = 1; e < kKeys; ++e)
+                mx = fmaxf(mx, s[e]);
+            mx *= a.scale_log2;  // scale > 0: the largest stays the largest
+            const float mn = mx > m + 8.f || m == -INFINITY ? fmaxf(mx, m) : m;
+            const float corr = mn == m ? 1.f : ex2(m - mn), ref = mn == -INFINITY ? 0.f : mn;
+            m = mn;
+            float sum = 0.f;
+#pragma unroll
+            for (int e = 0; e < kKeys; ++e) {
+                s[e] = ex2(fmaf(s[e], a.scale_log2, -ref));
+                sum += s[e];
+            }
+            l = fmaf(l, corr, sum);
+            if (i > 0 && !warp_wait(o_done, (i - 1) & 1, fail)) {  // O is whole, P has been read
+                ok = false;
+                break;
+            }
+            if (i > 0 && __any_sync(0xffffffffu, corr != 1.f)) {
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < HD; c += 16) {
+                    float o[16];
+                    tmem_ld16(tmem + lanes + 128 + c, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        o[e] *= corr;
+                    tmem_st16(tmem + lanes + 128 + c, o);
+                }
+                tmem_st_wait();
+            }
+#pragma unroll
+            for (int c = 0; c < kKeys / 8; ++c)
+                sts128(ps + r * 128 + ((c ^ (r & 7)) << 4), f2_bf16(s[8 * c], s[8 * c + 1]),
+                       f2_bf16(s[8 * c + 2], s[8 * c + 3]), f2_bf16(s[8 * c + 4], s[8 * c + 5]),
+                       f2_bf16(s[8 * c + 6], s[8 * c + 7]));
+            fence_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(p_full);
+        }
+        if (ok && tn > 0 && warp_wait(o_done, (tn - 1) & 1, fail)) {
+            tc_fence_after();
+            const float inv = 1.f / l;
+            uint16_t *out = a.out + tok * a.o_ts + h * a.o_hs;
+            const bool wide = ((uintptr_t)out & 15) == 0;
+            bool finite = true;
+#pragma unroll
+            for (int c = 0; c < HD; c += 16) {
+                float o[16];
+                tmem_ld16(tmem + lanes + 128 + c, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    o[e] *= inv;
+                    finite &= c + e >= a.hd || fabsf(o[e]) < INFINITY;
+                }
+                if (in && wide && c + 16 <= a.hd) {
+#pragma unroll
+                    for (int e = 0; e < 16; e += 8)
+                        *reinterpret_cast<uint4 *>(out + c + e) = make_uint4(
+                            f2_bf16(o[e], o[e + 1]), f2_bf16(o[e + 2], o[e + 3]),
+                            f2_bf16(o[e + 4], o[e + 5]), f2_bf16(o[e + 6], o[e + 7]));
+                } else if (in) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (c + e < a.hd)
+                            out[c + e] = f_bf16(o[e]);
+                }
+            }
+            // rows that are not finite again, by the warp (P has been read: its
+            // memory takes the queries)
+            uint32_t again = __ballot_sync(0xffffffffu, in && !finite);
+            float *qrow = reinterpret_cast<float *>(smem + (ps - base)) + (warp - 4) * kMaxHd;
+            while (again) {
+                const int src = __ffs(again) - 1;
+                again &= again - 1;
+                const int t1 = __shfl_sync(0xffffffffu, tok, src);
+                const int h1 = __shfl_sync(0xffffffffu, h, src);
+                const uint16_t *q = a.q + t1 * a.q_ts + h1 * a.q_hs;
+                __syncwarp();
+                for (int d = lane; d < a.hd; d += 32)
+                    qrow[d] = bf16f(q[d]) * a.scale_log2;
+                __syncwarp();
+                attend_row(a, t1, h1, qrow, [](int) { return true; });
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0 && *fail)
+        atomicAdd(&g_timeouts, 1u);
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc<C::COLS>(tmem);
+    }
+}
+
+template <int HD>
+cudaError_t launch_tc(TileParams &p, cudaStream_t stream)
+{
+    using C = TcCfg<HD>;
+    p.tiles = (p.rows + 127) / 128;
+    p.split = 1;
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e =
+        allow_once(allowed, reinterpret_cast<const void *>(attn_tc<HD>), C::SMEM);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((int64_t)p.tiles * p.n_kv));
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_tc<HD>, p);
+}
+
 template <int HD>
 cudaError_t launch_hd(TileParams &p, cudaStream_t stream)
 {
     const int64_t wide = (int64_t)((p.rows + 127) / 128) * p.n_kv;
+    const AttnParams &a = p.a;
+    if (p.rows >= 128 && aligned(a.q, 16) && a.q_ts % 8 == 0 && a.q_hs % 8 == 0)
+        return launch_tc<HD>(p, stream);
     if (p.rows <= 16)
         return launch_tiles<HD, 1, 4>(p, stream);
     if (p.rows <= 32)

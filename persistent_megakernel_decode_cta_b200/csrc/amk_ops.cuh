@@ -185,6 +185,13 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t smem)
     return (uint64_t)((smem >> 4) & 0x3fff) | (1ull << 16) | (64ull << 32) | (1ull << 46) |
            (2ull << 61);
 }
+// The same of an operand whose rows are K: blocks of 64 of its M or N elements
+// (a swizzled row each), `pitch` bytes apart, eight rows to a 1024-byte atom.
+__device__ __forceinline__ uint64_t tc_desc_mn(uint32_t smem, uint32_t pitch)
+{
+    return (uint64_t)((smem >> 4) & 0x3fff) | ((uint64_t)(pitch >> 4) << 16) | (64ull << 32) |
+           (1ull << 46) | (2ull << 61);
+}
 // Instruction descriptor: fp32 accumulators, bf16 A and B, both K-major (B
 // transposed when b_mn: its rows are K), M x N.
 __device__ __forceinline__ constexpr uint32_t tc_idesc(int m, int n, bool b_mn = false)
