@@ -16,6 +16,7 @@ struct AttnParams {
     uint16_t *out;
     int64_t q_ts, q_hs, o_ts, o_hs, k_hs, k_rs, v_hs, v_rs;
     int32_t T, pos, n_heads, group, hd, window, sinks;
+    int32_t q_pairs;   // q can be read two elements at a time
     float scale_log2;  // scale * log2(e): weights are 2^(s - m)
 };
 
@@ -114,8 +115,8 @@ __device__ unsigned int g_timeouts;  // CTAs that gave up a wait
 // group's heads and neighbouring tokens share every K and V row that is read.
 // A producer warp streams the visible K and V rows, 64 at a time, through a
 // ring of stages with TMA (swizzled; rows behind the last token and elements
-// behind head_dim read as 0); WM x WK warps take 16 rows each and a WK-th of
-// the stage's keys: scores, the running maximum and sum of the softmax, and
+// behind head_dim read as 0); GR groups of WM x WK warps take the stages by
+// turns, a warp 16 rows and a WK-th of the stage's keys: scores, the running maximum and sum of the softmax, and
 // the weighted sum of V, all in registers (weights are rounded to bf16 for the
 // product with V, as tensor cores take them: 2^-9 of each; their sum is taken
 // before).  The warps that share rows merge through shared memory, the CTAs of
@@ -134,25 +135,27 @@ struct TileParams {
     int32_t tiles, n_kv, split;
 };
 
-template <int HD, int WM, int WK>
+template <int HD, int WM, int WK, int GR>
 struct TileCfg {
     static constexpr int ROWS = 16 * WM, KW = kKeys / WK;
-    static constexpr int WARPS = WM * WK, THREADS = 32 * (WARPS + 1);
+    static constexpr int GROUP = WM * WK, WARPS = GROUP * GR, THREADS = 32 * (WARPS + 1);
+    static constexpr int PARTS = WK * GR;  // warps that share a row
     static constexpr int STAGE = 2 * kKeys * HD * 2;
-    // two CTAs to an SM, but for the widest tiles of the widest heads
-    static constexpr int CTAS = HD == 128 && WM == 8 ? 1 : 2;
+    // two CTAs to an SM where their registers fit (168 a thread of the wide
+    // heads, 112 else)
+    static constexpr int CTAS = THREADS * (HD == 128 ? 168 : 112) * 2 <= 65536 ? 2 : 1;
     static constexpr int STAGES = (CTAS == 1 ? 192 : 96) * 1024 / STAGE;
     static constexpr int OS = HD + 8;  // floats of a row of sums (padded)
     static constexpr int SMEM = STAGES * STAGE + 1024;
-    static_assert(WK * ROWS * (OS + 2) * 4 + ROWS * 8 + WARPS * kMaxHd * 4 <= STAGES * STAGE,
+    static_assert(PARTS * ROWS * (OS + 2) * 4 + ROWS * 8 + WARPS * kMaxHd * 4 <= STAGES * STAGE,
                   "the sums reuse the ring");
 };
 
-template <int HD, int WM, int WK>
-__global__ void __launch_bounds__(TileCfg<HD, WM, WK>::THREADS, (TileCfg<HD, WM, WK>::CTAS))
+template <int HD, int WM, int WK, int GR>
+__global__ void __launch_bounds__(TileCfg<HD, WM, WK, GR>::THREADS, (TileCfg<HD, WM, WK, GR>::CTAS))
     attn_tiles(const __grid_constant__ TileParams p)
 {
-    using C = TileCfg<HD, WM, WK>;
+    using C = TileCfg<HD, WM, WK, GR>;
     constexpr int KW = C::KW;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[2 * C::STAGES];
@@ -167,7 +170,7 @@ __global__ void __launch_bounds__(TileCfg<HD, WM, WK>::THREADS, (TileCfg<HD, WM,
         fail_flag = 0;
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(full(s), 1);
-            mbar_init(empty(s), C::WARPS);
+            mbar_init(empty(s), C::GROUP);
         }
         mbar_init_fence();
         prefetch_map(&p.k);
@@ -224,7 +227,8 @@ __global__ void __launch_bounds__(TileCfg<HD, WM, WK>::THREADS, (TileCfg<HD, WM,
                 }
             }
     } else {
-        const int wm = warp % WM, wk = warp / WM, g = lane >> 2, t = lane & 3;
+        const int grp = warp / C::GROUP, wm = warp % WM, wk = warp % C::GROUP / WM;
+        const int g = lane >> 2, t = lane & 3;
         // rows g and g + 8 of the warp's 16
         int prow[2];
         uint32_t qf[HD / 16][4];
@@ -240,16 +244,20 @@ __global__ void __launch_bounds__(TileCfg<HD, WM, WK>::THREADS, (TileCfg<HD, WM,
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const int d = i * 16 + c * 8 + 2 * t;
-                    const uint32_t x0 = in && d < a.hd ? q[d] : 0;
-                    const uint32_t x1 = in && d + 1 < a.hd ? q[d + 1] : 0;
-                    qf[i][h + 2 * c] = x0 | (x1 << 16);
+                    if (a.q_pairs) {
+                        qf[i][h + 2 * c] =
+                            in && d < a.hd ? __ldg(reinterpret_cast<const uint32_t *>(q + d)) : 0;
+                    } else {
+                        const uint32_t x0 = in && d < a.hd ? q[d] : 0;
+                        const uint32_t x1 = in && d + 1 < a.hd ? q[d + 1] : 0;
+                        qf[i][h + 2 * c] = x0 | (x1 << 16);
+                    }
                 }
         }
         float o[HD / 8][4] = {}, m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-        uint32_t ph = 0;
-        int s = 0;
-        for (int i = t0; i < t1; ++i) {
-            if (!warp_wait(full(s), ph, fail))
+        for (int i = t0 + grp; i < t1; i += GR) {
+            const int s = (i - t0) % C::STAGES;
+            if (!warp_wait(full(s), ((i - t0) / C::STAGES) & 1, fail))
                 break;
             const int j0 = (i < ta ? i * kKeys : lo + (i - ta) * kKeys) + wk * KW;
             const uint32_t ks = ring + s * C::STAGE + wk * KW * 128, vs = ks + C::STAGE / 2;
@@ -332,10 +340,6 @@ __global__ void __launch_bounds__(TileCfg<HD, WM, WK>::THREADS, (TileCfg<HD, WM,
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(empty(s));
-            if (++s == C::STAGES) {
-                s = 0;
-                ph ^= 1;
-            }
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -344,10 +348,10 @@ __global__ void __launch_bounds__(TileCfg<HD, WM, WK>::THREADS, (TileCfg<HD, WM,
         }
         named_bar(1, C::WARPS * 32);  // every warp has read its last stage
         float *os = reinterpret_cast<float *>(smem_raw + (ring - smem_u32(smem_raw)));
-        float *ml = os + WK * C::ROWS * C::OS;
+        float *ml = os + C::PARTS * C::ROWS * C::OS;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int r = wk * C::ROWS + wm * 16 + g + 8 * h;
+            const int r = (grp * WK + wk) * C::ROWS + wm * 16 + g + 8 * h;
 #pragma unroll
             for (int d = 0; d < HD / 8; ++d)
                 *reinterpret_cast<float2 *>(os + r * C::OS + d * 8 + 2 * t) =
@@ -361,7 +365,7 @@ __global__ void __launch_bounds__(TileCfg<HD, WM, WK>::THREADS, (TileCfg<HD, WM,
     }
     // merge: over the warps of a row, then over the cluster's CTAs
     float *os = reinterpret_cast<float *>(smem_raw + (ring - smem_u32(smem_raw)));
-    float *ml = os + WK * C::ROWS * C::OS, *mc = ml + 2 * WK * C::ROWS;
+    float *ml = os + C::PARTS * C::ROWS * C::OS, *mc = ml + 2 * C::PARTS * C::ROWS;
     const int hd = a.hd, nt = C::WARPS * 32;
     auto weigh = [](float m, float M) { return m == -INFINITY ? 0.f : ex2(m - M); };
     auto put = [&](int r, int d, float v) {
@@ -378,10 +382,10 @@ __global__ void __launch_bounds__(TileCfg<HD, WM, WK>::THREADS, (TileCfg<HD, WM,
                 const int r = i / hd, d = i - r * hd;
                 float M = -INFINITY, L = 0.f, O = 0.f;
 #pragma unroll
-                for (int k = 0; k < WK; ++k)
+                for (int k = 0; k < C::PARTS; ++k)
                     M = fmaxf(M, ml[2 * (k * C::ROWS + r)]);
 #pragma unroll
-                for (int k = 0; k < WK; ++k) {
+                for (int k = 0; k < C::PARTS; ++k) {
                     const int at = k * C::ROWS + r;
                     const float w = weigh(ml[2 * at], M);
                     L = fmaf(ml[2 * at + 1], w, L);
@@ -396,10 +400,10 @@ __global__ void __launch_bounds__(TileCfg<HD, WM, WK>::THREADS, (TileCfg<HD, WM,
                 const int r = i / hd, d = i - r * hd;
                 float M = -INFINITY, L = 0.f, O = 0.f;
 #pragma unroll
-                for (int k = 0; k < WK; ++k)
+                for (int k = 0; k < C::PARTS; ++k)
                     M = fmaxf(M, ml[2 * (k * C::ROWS + r)]);
 #pragma unroll
-                for (int k = 0; k < WK; ++k) {
+                for (int k = 0; k < C::PARTS; ++k) {
                     const int at = k * C::ROWS + r;
                     const float w = weigh(ml[2 * at], M);
                     L = fmaf(ml[2 * at + 1], w, L);
@@ -468,10 +472,10 @@ __global__ void __launch_bounds__(TileCfg<HD, WM, WK>::THREADS, (TileCfg<HD, WM,
         atomicAdd(&g_timeouts, 1u);
 }
 
-template <int HD, int WM, int WK>
+template <int HD, int WM, int WK, int GR>
 cudaError_t launch_tiles(TileParams &p, cudaStream_t stream)
 {
-    using C = TileCfg<HD, WM, WK>;
+    using C = TileCfg<HD, WM, WK, GR>;
     p.tiles = (p.rows + C::ROWS - 1) / C::ROWS;
     const AttnParams &a = p.a;
     // keys of the longest tile, in stages; the CTAs of a cluster share them, as
@@ -486,7 +490,7 @@ cudaError_t launch_tiles(TileParams &p, cudaStream_t stream)
         p.split *= 2;
     if (base * p.split > INT32_MAX)
         return cudaErrorInvalidValue;
-    auto kernel = attn_tiles<HD, WM, WK>;
+    auto kernel = attn_tiles<HD, WM, WK, GR>;
     static std::atomic<uint64_t> allowed{0};
     const cudaError_t e =
         allow_once(allowed, reinterpret_cast<const void *>(kernel), C::SMEM, true);
@@ -850,17 +854,14 @@ cudaError_t launch_tc(TileParams &p, cudaStream_t stream)
 template <int HD>
 cudaError_t launch_hd(TileParams &p, cudaStream_t stream)
 {
-    const int64_t wide = (int64_t)((p.rows + 127) / 128) * p.n_kv;
     const AttnParams &a = p.a;
     if (p.rows >= 128 && aligned(a.q, 16) && a.q_ts % 8 == 0 && a.q_hs % 8 == 0)
         return launch_tc<HD>(p, stream);
     if (p.rows <= 16)
-        return launch_tiles<HD, 1, 4>(p, stream);
+        return launch_tiles<HD, 1, 4, HD == 64 ? 2 : 1>(p, stream);
     if (p.rows <= 32)
-        return launch_tiles<HD, 2, 2>(p, stream);
-    if (wide < sm_count())
-        return launch_tiles<HD, 4, 1>(p, stream);
-    return launch_tiles<HD, 8, 1>(p, stream);
+        return launch_tiles<HD, 2, 4, 1>(p, stream);
+    return launch_tiles<HD, 4, HD == 64 ? 4 : 2, 1>(p, stream);
 }
 
 // Whether TMA can read the cache rows: 16-byte strides and bases.
@@ -950,6 +951,7 @@ extern "C" int amk_attention(const amk_attention_args *a, void *cuda_stream)
     p.n_heads = a->n_heads;
     p.group = a->n_heads / a->n_kv_heads;
     p.hd = a->head_dim;
+    p.q_pairs = aligned(a->q, 4) && p.q_ts % 2 == 0 && p.q_hs % 2 == 0 && p.hd % 2 == 0;
     p.window = a->window;
     p.sinks = a->sinks;
     p.scale_log2 = (a->scale > 0.f ? a->scale : 1.f / sqrtf((float)a->head_dim)) * 1.4426950408889634f;
