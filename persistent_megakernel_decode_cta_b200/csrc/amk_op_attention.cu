@@ -111,17 +111,22 @@ __global__ void __launch_bounds__(128) attn_rows(const AttnParams a)
 __device__ unsigned int g_timeouts;  // CTAs that gave up a wait
 
 // ---- tiles of rows ---------------------------------------------------------------
-// The (token, head) pairs of a KV head are the rows of tiles of 16 WM: a
-// group's heads and neighbouring tokens share every K and V row that is read.
-// A producer warp streams the visible K and V rows, 64 at a time, through a
-// ring of stages with TMA (swizzled; rows behind the last token and elements
-// behind head_dim read as 0); GR groups of WM x WK warps take the stages by
-// turns, a warp 16 rows and a WK-th of the stage's keys: scores, the running maximum and sum of the softmax, and
-// the weighted sum of V, all in registers (weights are rounded to bf16 for the
-// product with V, as tensor cores take them: 2^-9 of each; their sum is taken
-// before).  The warps that share rows merge through shared memory, the CTAs of
-// a cluster that share the keys of a tile through distributed shared memory,
-// in a fixed order.
+// The (token, head) pairs of a KV head are the rows of tiles of 16: a group's
+// heads and neighbouring tokens share every K and V row that is read.  A
+// producer warp streams the visible K and V rows, 64 at a time, through a ring
+// of stages with TMA (swizzled; rows behind the last token and elements behind
+// head_dim read as 0); GR groups of WK warps take the stages by turns, a warp
+// the tile's 16 rows and a WK-th of the stage's keys: scores, the running
+// maximum and sum of the softmax, and the weighted sum of V, all in registers
+// (weights are rounded to bf16 for the product with V, as tensor cores take
+// them: 2^-9 of each; their sum is taken before).  The warps merge through
+// shared memory, the CTAs of a cluster that share the keys of a tile through
+// distributed shared memory, in a fixed order.
+//
+// A step of a warp is a chain of dependent instructions (0.4 us for 16 keys),
+// so what counts is how many of them run at once: tiles of 32 or 64 rows, with
+// as many warps, took 28 and 30 us where these take 19 (5 tokens, 32 heads on
+// 4, 32000 rows of 64).
 //
 // A masked weight is 0, and 0 times a NaN or infinity in a masked V row is
 // NaN.  So where a result is not finite its row is computed again by
@@ -135,27 +140,121 @@ struct TileParams {
     int32_t tiles, n_kv, split;
 };
 
-template <int HD, int WM, int WK, int GR>
+__device__ __forceinline__ float weigh(float m, float M)
+{
+    return m == -INFINITY ? 0.f : ex2(m - M);
+}
+// Element d of a tile's row r, unless it is not finite: the row is then noted.
+__device__ __forceinline__ void put(const TileParams &p, int r0, int kvh, int r, int d, float v,
+                                    int *redo)
+{
+    if (!(fabsf(v) < INFINITY)) {
+        redo[r] = 1;
+        return;
+    }
+    const AttnParams &a = p.a;
+    const int row = r0 + r;
+    a.out[(row / a.group) * a.o_ts + (kvh * a.group + row % a.group) * a.o_hs + d] = f_bf16(v);
+}
+// Merges the sums os [rows][OS] and their (maximum, sum) ml [rows][2] of a
+// cluster's CTAs, in the ranks' order; this rank's share of the elements, four
+// at a time, by thread idx of nt.  A cluster barrier before and after.
+template <int OS>
+__device__ __forceinline__ void merge_cluster(const TileParams &p, uint32_t os, uint32_t ml, int r0,
+                                              int nrows, int kvh, int rank, int idx, int nt,
+                                              int *redo)
+{
+    const int hd = p.a.hd, split = p.split, quads = (hd + 3) / 4;
+    for (int i = rank * nt + idx; i < nrows * quads; i += split * nt) {
+        const int r = i / quads, d = (i - r * quads) * 4;
+        float M = -INFINITY, L = 0.f, O[4] = {};
+        for (int k0 = 0; k0 < split; k0 += 4) {  // four CTAs' partials at a time
+            float2 w[4];
+            float4 o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int kk = min(k0 + k, split - 1);
+                w[k] = ld_cluster2(map_rank(ml + r * 8, kk));
+                o[k] = ld_cluster4(map_rank(os + (r * OS + d) * 4, kk));
+            }
+            float Mn = M;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                Mn = fmaxf(Mn, w[k].x);  // the last one twice does no harm here
+            const float c = weigh(M, Mn);
+            L *= c;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                O[e] *= c;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float f = k0 + k < split ? weigh(w[k].x, Mn) : 0.f;
+                if (k0 + k < split) {
+                    L = fmaf(w[k].y, f, L);
+                    O[0] = fmaf(o[k].x, f, O[0]);
+                    O[1] = fmaf(o[k].y, f, O[1]);
+                    O[2] = fmaf(o[k].z, f, O[2]);
+                    O[3] = fmaf(o[k].w, f, O[3]);
+                }
+            }
+            M = Mn;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (d + e < hd)
+                put(p, r0, kvh, r, d + e, O[e] / L, redo);
+    }
+}
+// The noted rows again, by warps first, first + n, ...: this rank's share of
+// their elements.  qs: the warp's own kMaxHd floats.
+__device__ __forceinline__ void redo_rows(const TileParams &p, const int *redo, int r0, int nrows,
+                                          int kvh, int rank, int nt, int first, int n, float *qs)
+{
+    const AttnParams &a = p.a;
+    const int lane = threadIdx.x & 31;
+    for (int r = first; r < nrows; r += n)
+        if (redo[r]) {
+            const int row = r0 + r, tok = row / a.group, h = kvh * a.group + row % a.group;
+            const uint16_t *q = a.q + tok * a.q_ts + h * a.q_hs;
+            for (int d = lane; d < a.hd; d += 32)
+                qs[d] = bf16f(q[d]) * a.scale_log2;
+            __syncwarp();
+            attend_row(a, tok, h, qs, [&](int d) {
+                return (r * ((a.hd + 3) / 4) + d / 4) / nt % p.split == rank;
+            });
+            __syncwarp();
+        }
+}
+// The stages of a tile's keys that this rank of its cluster takes: [t0, t1).
+__device__ __forceinline__ void share(int stages, int rank, int split, int &t0, int &t1)
+{
+    t0 = (int)((int64_t)stages * rank / split);
+    t1 = (int)((int64_t)stages * (rank + 1) / split);
+}
+
+template <int HD, int WK, int GR>
 struct TileCfg {
-    static constexpr int ROWS = 16 * WM, KW = kKeys / WK;
-    static constexpr int GROUP = WM * WK, WARPS = GROUP * GR, THREADS = 32 * (WARPS + 1);
-    static constexpr int PARTS = WK * GR;  // warps that share a row
+    static constexpr int ROWS = 16, KW = kKeys / WK;
+    static constexpr int WARPS = WK * GR, THREADS = 32 * (WARPS + 1);
     static constexpr int STAGE = 2 * kKeys * HD * 2;
     // two CTAs to an SM where their registers fit (168 a thread of the wide
     // heads, 112 else)
     static constexpr int CTAS = THREADS * (HD == 128 ? 168 : 112) * 2 <= 65536 ? 2 : 1;
     static constexpr int STAGES = (CTAS == 1 ? 192 : 96) * 1024 / STAGE;
+    // a group waits for its next use of a stage by that use's parity: the one
+    // before must have been its own, or it could take an older phase for it
+    static_assert(STAGES % GR == 0, "a stage belongs to one group");
     static constexpr int OS = HD + 8;  // floats of a row of sums (padded)
     static constexpr int SMEM = STAGES * STAGE + 1024;
-    static_assert(PARTS * ROWS * (OS + 2) * 4 + ROWS * 8 + WARPS * kMaxHd * 4 <= STAGES * STAGE,
+    static_assert(WARPS * ROWS * (OS + 2) * 4 + ROWS * 8 + WARPS * kMaxHd * 4 <= STAGES * STAGE,
                   "the sums reuse the ring");
 };
 
-template <int HD, int WM, int WK, int GR>
-__global__ void __launch_bounds__(TileCfg<HD, WM, WK, GR>::THREADS, (TileCfg<HD, WM, WK, GR>::CTAS))
+template <int HD, int WK, int GR>
+__global__ void __launch_bounds__(TileCfg<HD, WK, GR>::THREADS, (TileCfg<HD, WK, GR>::CTAS))
     attn_tiles(const __grid_constant__ TileParams p)
 {
-    using C = TileCfg<HD, WM, WK, GR>;
+    using C = TileCfg<HD, WK, GR>;
     constexpr int KW = C::KW;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[2 * C::STAGES];
@@ -170,7 +269,7 @@ __global__ void __launch_bounds__(TileCfg<HD, WM, WK, GR>::THREADS, (TileCfg<HD,
         fail_flag = 0;
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(full(s), 1);
-            mbar_init(empty(s), C::GROUP);
+            mbar_init(empty(s), WK);
         }
         mbar_init_fence();
         prefetch_map(&p.k);
@@ -189,7 +288,8 @@ __global__ void __launch_bounds__(TileCfg<HD, WM, WK, GR>::THREADS, (TileCfg<HD,
     int na, lo;
     visible(a, pmin, na, lo);
     const int ta = (na + kKeys - 1) / kKeys, tn = ta + (pmax - lo + kKeys) / kKeys;
-    const int t0 = (int)((int64_t)tn * rank / split), t1 = (int)((int64_t)tn * (rank + 1) / split);
+    int t0, t1;
+    share(tn, rank, split, t0, t1);
     pdl_wait();
     pdl_launch();
     if (warp == C::WARPS) {
@@ -227,14 +327,14 @@ __global__ void __launch_bounds__(TileCfg<HD, WM, WK, GR>::THREADS, (TileCfg<HD,
                 }
             }
     } else {
-        const int grp = warp / C::GROUP, wm = warp % WM, wk = warp % C::GROUP / WM;
+        const int grp = warp / WK, wk = warp % WK;
         const int g = lane >> 2, t = lane & 3;
-        // rows g and g + 8 of the warp's 16
+        // the lane's rows: g and g + 8
         int prow[2];
         uint32_t qf[HD / 16][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int r = r0 + wm * 16 + g + 8 * h;
+            const int r = r0 + g + 8 * h;
             const bool in = r < p.rows;
             const int tok = in ? r / a.group : 0, hh = in ? r % a.group : 0;
             prow[h] = in ? a.pos + tok : pmax;
@@ -348,10 +448,10 @@ __global__ void __launch_bounds__(TileCfg<HD, WM, WK, GR>::THREADS, (TileCfg<HD,
         }
         named_bar(1, C::WARPS * 32);  // every warp has read its last stage
         float *os = reinterpret_cast<float *>(smem_raw + (ring - smem_u32(smem_raw)));
-        float *ml = os + C::PARTS * C::ROWS * C::OS;
+        float *ml = os + C::WARPS * C::ROWS * C::OS;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int r = (grp * WK + wk) * C::ROWS + wm * 16 + g + 8 * h;
+            const int r = warp * C::ROWS + g + 8 * h;
 #pragma unroll
             for (int d = 0; d < HD / 8; ++d)
                 *reinterpret_cast<float2 *>(os + r * C::OS + d * 8 + 2 * t) =
@@ -365,132 +465,85 @@ __global__ void __launch_bounds__(TileCfg<HD, WM, WK, GR>::THREADS, (TileCfg<HD,
     }
     // merge: over the warps of a row, then over the cluster's CTAs
     float *os = reinterpret_cast<float *>(smem_raw + (ring - smem_u32(smem_raw)));
-    float *ml = os + C::PARTS * C::ROWS * C::OS, *mc = ml + 2 * C::PARTS * C::ROWS;
+    float *ml = os + C::WARPS * C::ROWS * C::OS, *mc = ml + 2 * C::WARPS * C::ROWS;
     const int hd = a.hd, nt = C::WARPS * 32;
-    auto weigh = [](float m, float M) { return m == -INFINITY ? 0.f : ex2(m - M); };
-    auto put = [&](int r, int d, float v) {
-        if (!(fabsf(v) < INFINITY)) {
-            redo[r] = 1;
-            return;
-        }
-        const int row = r0 + r;
-        a.out[(row / a.group) * a.o_ts + (kvh * a.group + row % a.group) * a.o_hs + d] = f_bf16(v);
-    };
-    if (split == 1) {
-        if (tid < nt && !*fail)
-            for (int i = tid; i < nrows * hd; i += nt) {
-                const int r = i / hd, d = i - r * hd;
-                float M = -INFINITY, L = 0.f, O = 0.f;
+    const int quads = (hd + 3) / 4;
+    if (tid < nt && !*fail)
+        for (int i = tid; i < nrows * quads; i += nt) {
+            const int r = i / quads, d = (i - r * quads) * 4;
+            float2 w[C::WARPS];
+            float M = -INFINITY, L = 0.f, O[4] = {};
 #pragma unroll
-                for (int k = 0; k < C::PARTS; ++k)
-                    M = fmaxf(M, ml[2 * (k * C::ROWS + r)]);
-#pragma unroll
-                for (int k = 0; k < C::PARTS; ++k) {
-                    const int at = k * C::ROWS + r;
-                    const float w = weigh(ml[2 * at], M);
-                    L = fmaf(ml[2 * at + 1], w, L);
-                    O = fmaf(os[at * C::OS + d], w, O);
-                }
-                put(r, d, O / L);
+            for (int k = 0; k < C::WARPS; ++k) {
+                w[k] = *reinterpret_cast<const float2 *>(ml + 2 * (k * C::ROWS + r));
+                M = fmaxf(M, w[k].x);
             }
-        __syncthreads();
-    } else {
-        if (tid < nt) {
-            for (int i = tid; i < nrows * hd; i += nt) {
-                const int r = i / hd, d = i - r * hd;
-                float M = -INFINITY, L = 0.f, O = 0.f;
 #pragma unroll
-                for (int k = 0; k < C::PARTS; ++k)
-                    M = fmaxf(M, ml[2 * (k * C::ROWS + r)]);
+            for (int k = 0; k < C::WARPS; ++k) {
+                const float4 o =
+                    *reinterpret_cast<const float4 *>(os + (k * C::ROWS + r) * C::OS + d);
+                const float f = weigh(w[k].x, M);
+                L = fmaf(w[k].y, f, L);
+                O[0] = fmaf(o.x, f, O[0]);
+                O[1] = fmaf(o.y, f, O[1]);
+                O[2] = fmaf(o.z, f, O[2]);
+                O[3] = fmaf(o.w, f, O[3]);
+            }
+            if (split == 1) {
 #pragma unroll
-                for (int k = 0; k < C::PARTS; ++k) {
-                    const int at = k * C::ROWS + r;
-                    const float w = weigh(ml[2 * at], M);
-                    L = fmaf(ml[2 * at + 1], w, L);
-                    O = fmaf(os[at * C::OS + d], w, O);
-                }
-                os[r * C::OS + d] = O;
+                for (int e = 0; e < 4; ++e)
+                    if (d + e < hd)
+                        put(p, r0, kvh, r, d + e, O[e] / L, redo);
+            } else {
+                *reinterpret_cast<float4 *>(os + r * C::OS + d) =
+                    make_float4(O[0], O[1], O[2], O[3]);
                 if (d == 0) {
                     mc[2 * r] = M;
                     mc[2 * r + 1] = L;
                 }
             }
         }
+    if (split == 1) {
+        __syncthreads();
+    } else {
         cluster_sync();
-        if (tid < nt && !*fail) {
-            const uint32_t oa = smem_u32(os), ma = smem_u32(mc);
-            for (int i = rank * nt + tid; i < nrows * hd; i += split * nt) {
-                const int r = i / hd, d = i - r * hd;
-                float M = -INFINITY, L = 0.f, O = 0.f;
-                for (int k0 = 0; k0 < split; k0 += 4) {  // four CTAs' partials at a time
-                    float mk[4], lk[4], ok[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const bool in = k0 + k < split;
-                        const int kk = in ? k0 + k : 0;
-                        const float x = ld_cluster(map_rank(ma + r * 8, kk));
-                        mk[k] = in ? x : -INFINITY;
-                        lk[k] = ld_cluster(map_rank(ma + r * 8 + 4, kk));
-                        ok[k] = ld_cluster(map_rank(oa + (r * C::OS + d) * 4, kk));
-                    }
-                    float Mn = M;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        Mn = fmaxf(Mn, mk[k]);
-                    const float c = weigh(M, Mn);
-                    L *= c;
-                    O *= c;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float w = weigh(mk[k], Mn);
-                        L = fmaf(lk[k], w, L);
-                        O = fmaf(ok[k], w, O);
-                    }
-                    M = Mn;
-                }
-                put(r, d, O / L);
-            }
-        }
+        if (tid < nt && !*fail)
+            merge_cluster<C::OS>(p, smem_u32(os), smem_u32(mc), r0, nrows, kvh, rank, tid, nt, redo);
         cluster_sync();  // no CTA leaves, or writes below, while another reads
     }
-    if (warp < C::WARPS) {
-        float *qs = mc + 2 * C::ROWS + warp * kMaxHd;
-        for (int r = warp; r < nrows; r += C::WARPS)
-            if (redo[r]) {
-                const int row = r0 + r, tok = row / a.group, h = kvh * a.group + row % a.group;
-                const uint16_t *q = a.q + tok * a.q_ts + h * a.q_hs;
-                for (int d = lane; d < hd; d += 32)
-                    qs[d] = bf16f(q[d]) * a.scale_log2;
-                __syncwarp();
-                attend_row(a, tok, h, qs, [&](int d) {  // this CTA's share of the row
-                    return ((r * hd + d) / nt) % split == rank;
-                });
-                __syncwarp();
-            }
-    }
+    if (warp < C::WARPS)
+        redo_rows(p, redo, r0, nrows, kvh, rank, nt, warp, C::WARPS,
+                  mc + 2 * C::ROWS + warp * kMaxHd);
     if (tid == 0 && *fail)
         atomicAdd(&g_timeouts, 1u);
 }
 
-template <int HD, int WM, int WK, int GR>
-cudaError_t launch_tiles(TileParams &p, cudaStream_t stream)
+// CTAs of a cluster that share a tile's keys: as many as all run at once and
+// have `least` stages each (the longest tile's) to read.
+int choose_split(const TileParams &p, int tile_rows, int ctas, int least)
 {
-    using C = TileCfg<HD, WM, WK, GR>;
-    p.tiles = (p.rows + C::ROWS - 1) / C::ROWS;
     const AttnParams &a = p.a;
-    // keys of the longest tile, in stages; the CTAs of a cluster share them, as
-    // many as run at once and have two stages to read
-    const int last = a.pos + a.T - 1, first = a.pos + (p.tiles - 1) * C::ROWS / a.group;
+    const int last = a.pos + a.T - 1, first = a.pos + (p.tiles - 1) * tile_rows / a.group;
     const int lo = a.window && first - a.window + 1 > 0 ? first - a.window + 1 : 0;
     const int sinks = a.sinks < lo ? a.sinks : lo;
     const int64_t stages = (sinks + kKeys - 1) / kKeys + ((int64_t)last - lo + kKeys) / kKeys;
-    const int64_t base = (int64_t)p.tiles * p.n_kv, room = (int64_t)sm_count() * C::CTAS;
-    p.split = 1;
-    while (p.split < 16 && base * p.split * 2 <= room && stages >= 4 * p.split)
-        p.split *= 2;
+    const int64_t base = (int64_t)p.tiles * p.n_kv, room = (int64_t)sm_count() * ctas;
+    int split = 1;
+    while (split < 16 && base * split * 2 <= room && stages >= 2 * least * split)
+        split *= 2;
+    return split;
+}
+
+template <int HD, int WK, int GR>
+cudaError_t launch_tiles(TileParams &p, cudaStream_t stream)
+{
+    using C = TileCfg<HD, WK, GR>;
+    p.tiles = (p.rows + C::ROWS - 1) / C::ROWS;
+    const int64_t base = (int64_t)p.tiles * p.n_kv;
+    p.split = choose_split(p, C::ROWS, C::CTAS, 2);
     if (base * p.split > INT32_MAX)
         return cudaErrorInvalidValue;
-    auto kernel = attn_tiles<HD, WM, WK, GR>;
+    auto kernel = attn_tiles<HD, WK, GR>;
     static std::atomic<uint64_t> allowed{0};
     const cudaError_t e =
         allow_once(allowed, reinterpret_cast<const void *>(kernel), C::SMEM, true);
@@ -513,7 +566,7 @@ cudaError_t launch_tiles(TileParams &p, cudaStream_t stream)
 }
 
 // ---- long prompts: tcgen05 --------------------------------------------------------
-// Tiles of 128 rows (as above), one CTA each, two CTAs to an SM so that one's
+// Tiles of 128 rows (as above), a CTA or a cluster each, two CTAs to an SM so that one's
 // products run under the other's softmax.  Both products run on tcgen05: S = Q
 // K^T into one of two TMEM buffers, O += P V into a third, with P through
 // shared memory in the layout the MMA reads, and V taken as it lies in the
@@ -527,7 +580,9 @@ struct TcCfg {
     static constexpr int SUB = HD / 64;               // blocks of 64 elements of a head
     static constexpr int Q = SUB * 128 * 128, KV = SUB * kKeys * 128, P = 128 * 128;
     static constexpr int BARS = Q + 4 * KV + P;       // two stages of K and of V
-    static constexpr int SMEM = BARS + 256;
+    static constexpr int SMEM = BARS + 256 + 512;
+    static constexpr int OS = HD + 4;                 // floats of a row of sums (padded)
+    static_assert(128 * OS * 4 + 128 * 8 + 4 * kMaxHd * 4 <= Q + 4 * KV + P, "the sums reuse it all");
     static constexpr int THREADS = 256, COLS = 256;   // TMEM: two S of 64 columns, O from 128 on
 };
 
@@ -549,7 +604,10 @@ __global__ void __launch_bounds__(TcCfg<HD>::THREADS, 2)
     auto s_free = [&](int b) { return bar0 + 104 + 8 * b; };
     int *flags = reinterpret_cast<int *>(smem + C::BARS + 128);  // TMEM address, failure
     volatile int *fail = flags + 1;
+    int *redo = reinterpret_cast<int *>(smem + C::BARS + 256);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid < 128)
+        redo[tid] = 0;
     if (tid == 0) {
         flags[1] = (base & 1023) != 0;  // the swizzled layouts count from 1024-byte boundaries
         mbar_init(q_full, 4);
@@ -574,14 +632,18 @@ __global__ void __launch_bounds__(TcCfg<HD>::THREADS, 2)
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(flags);
     const AttnParams &a = p.a;
-    const int kvh = blockIdx.x % p.n_kv;
-    const int r0 = (p.tiles - 1 - blockIdx.x / p.n_kv) * 128;  // the longest rows start first
+    const int split = p.split, rank = blockIdx.x % split;
+    const int rest = blockIdx.x / split, kvh = rest % p.n_kv;
+    const int r0 = (p.tiles - 1 - rest / p.n_kv) * 128;  // the longest rows start first
     const int nrows = min(128, p.rows - r0);
     const int pmin = a.pos + r0 / a.group, pmax = a.pos + (r0 + nrows - 1) / a.group;
     int na, lo;
     visible(a, pmin, na, lo);
-    const int ta = (na + kKeys - 1) / kKeys, tn = *fail ? 0 : ta + (pmax - lo + kKeys) / kKeys;
-    auto first_key = [&](int i) { return i < ta ? i * kKeys : lo + (i - ta) * kKeys; };
+    const int ta = (na + kKeys - 1) / kKeys;
+    int t0, t1;
+    share(ta + (pmax - lo + kKeys) / kKeys, rank, split, t0, t1);
+    const int tn = *fail ? 0 : t1 - t0;  // stages of this CTA
+    auto first_key = [&](int i) { return t0 + i < ta ? (t0 + i) * kKeys : lo + (t0 + i - ta) * kKeys; };
     pdl_wait();
     pdl_launch();
     if (warp == 0) {
@@ -713,7 +775,7 @@ __global__ void __launch_bounds__(TcCfg<HD>::THREADS, 2)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(s_free(b));
-            const bool sink = i < ta;
+            const bool sink = t0 + i < ta;
             if (sink ? j0 + kKeys > na
                      : j0 + kKeys - 1 > pmin || (a.window && j0 <= pmax - a.window)) {
                 // keys j0 + e of the row: e < hi, and e >= from or e < sinks
@@ -769,8 +831,30 @@ __global__ void __launch_bounds__(TcCfg<HD>::THREADS, 2)
             if (lane == 0)
                 mbar_arrive(p_full);
         }
-        if (ok && tn > 0 && warp_wait(o_done, (tn - 1) & 1, fail)) {
-            tc_fence_after();
+        if (ok && tn > 0)
+            ok = warp_wait(o_done, (tn - 1) & 1, fail);
+        tc_fence_after();
+        if (split > 1) {
+            // this rank's sums for the cluster; every copy and product that used
+            // the memory has finished (all four warps have seen the last one)
+            named_bar(1, 128);
+            float *os = reinterpret_cast<float *>(smem) + r * C::OS;
+            float *ml = reinterpret_cast<float *>(smem) + 128 * C::OS + 2 * r;
+            ml[0] = m;
+            ml[1] = l;
+#pragma unroll
+            for (int c = 0; c < HD; c += 16) {
+                float o[16] = {};
+                if (tn > 0) {
+                    tmem_ld16(tmem + lanes + 128 + c, o);
+                    tmem_ld_wait();
+                }
+#pragma unroll
+                for (int e = 0; e < 16; e += 4)
+                    *reinterpret_cast<float4 *>(os + c + e) =
+                        make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            }
+        } else if (ok) {
             const float inv = 1.f / l;
             uint16_t *out = a.out + tok * a.o_ts + h * a.o_hs;
             const bool wide = ((uintptr_t)out & 15) == 0;
@@ -818,6 +902,17 @@ __global__ void __launch_bounds__(TcCfg<HD>::THREADS, 2)
     }
     __syncwarp();
     tc_fence_before();
+    if (split > 1) {
+        cluster_sync();
+        const float *os = reinterpret_cast<const float *>(smem), *ml = os + 128 * C::OS;
+        if (!*fail)
+            merge_cluster<C::OS>(p, smem_u32(os), smem_u32(ml), r0, nrows, kvh, rank, tid,
+                                 C::THREADS, redo);
+        cluster_sync();  // no CTA leaves, or writes below, while another reads
+        if (warp >= 4)
+            redo_rows(p, redo, r0, nrows, kvh, rank, C::THREADS, warp - 4, 4,
+                      reinterpret_cast<float *>(smem) + (warp - 4) * kMaxHd);
+    }
     __syncthreads();
     if (tid == 0 && *fail)
         atomicAdd(&g_timeouts, 1u);
@@ -832,36 +927,43 @@ cudaError_t launch_tc(TileParams &p, cudaStream_t stream)
 {
     using C = TcCfg<HD>;
     p.tiles = (p.rows + 127) / 128;
-    p.split = 1;
+    p.split = choose_split(p, 128, 2, 8);
+    if ((int64_t)p.tiles * p.n_kv * p.split > INT32_MAX)
+        return cudaErrorInvalidValue;
     static std::atomic<uint64_t> allowed{0};
     const cudaError_t e =
-        allow_once(allowed, reinterpret_cast<const void *>(attn_tc<HD>), C::SMEM);
+        allow_once(allowed, reinterpret_cast<const void *>(attn_tc<HD>), C::SMEM, true);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((int64_t)p.tiles * p.n_kv));
+    cfg.gridDim = dim3((unsigned)((int64_t)p.tiles * p.n_kv * p.split));
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, attn_tc<HD>, p);
 }
 
 template <int HD>
 cudaError_t launch_hd(TileParams &p, cudaStream_t stream)
 {
+    // Tiles of 16 rows while an SM and a half have one each: beyond that the
+    // tensor cores' tiles of 128 (which want 16-byte query rows) read the cache
+    // so much less often that their longer steps are made up for.  Measured: 333
+    // tokens of 9 heads on 3 (189 tiles) 7.6 against 10.8 us, 128 tokens of 32
+    // heads over 2128 rows (256 tiles) 29.2 against 26.4.
     const AttnParams &a = p.a;
-    if (p.rows >= 128 && aligned(a.q, 16) && a.q_ts % 8 == 0 && a.q_hs % 8 == 0)
+    const int64_t small = (int64_t)((p.rows + 15) / 16) * p.n_kv;
+    if (2 * small > 3 * sm_count() && aligned(a.q, 16) && a.q_ts % 8 == 0 && a.q_hs % 8 == 0)
         return launch_tc<HD>(p, stream);
-    if (p.rows <= 16)
-        return launch_tiles<HD, 1, 4, HD == 64 ? 2 : 1>(p, stream);
-    if (p.rows <= 32)
-        return launch_tiles<HD, 2, 4, 1>(p, stream);
-    return launch_tiles<HD, 4, HD == 64 ? 4 : 2, 1>(p, stream);
+    return launch_tiles<HD, 4, HD == 64 ? 2 : 1>(p, stream);
 }
 
 // Whether TMA can read the cache rows: 16-byte strides and bases.
