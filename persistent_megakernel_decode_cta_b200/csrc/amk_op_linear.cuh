@@ -575,7 +575,11 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
     }
     __syncwarp();
     if (SPLIT) {
-        cluster_sync();  // every rank's sums are in its shared memory
+        // every rank's sums are in its shared memory
+        if (split == 1)
+            __syncthreads();
+        else
+            cluster_sync();
         const int et = tid - 128;
         if (et >= 0 && et < C::EW * 128 && !*fail) {
             const int tile = first;
@@ -587,29 +591,49 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
             uint32_t at[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                at[k] = map_rank(ring + (uint32_t)r * 4, k < split ? k : 0);
-            // added in the ranks' order: the same bits every time.  Four tokens at a
-            // time: one by one, a load's latency each was a third of a short call.
-            for (int c = et / rows; c < cols && n < p.e.n; c += 4 * dc) {
-                float s[4] = {}, u[4] = {};
+                at[k] = split == 1 ? ring + (uint32_t)r * 4
+                                   : map_rank(ring + (uint32_t)r * 4, k < split ? k : 0);
+            // added in the ranks' order: the same bits every time.  Several tokens at
+            // a time: one by one, a load's latency each was a third of a short call.
+            if (split == 1) {
+                for (int c = et / rows; c < cols && n < p.e.n; c += 8 * dc) {
+                    float s[8], u[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k < split) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {  // a token behind the last: the last again
-                            const uint32_t o = (uint32_t)min(c + i * dc, cols - 1) * 512;
-                            s[i] += ld_cluster(at[k] + o);
-                            if (gated)
-                                u[i] += ld_cluster(at[k] + o + 64 * 4);
-                        }
+                    for (int i = 0; i < 8; ++i) {  // a token behind the last: the last again
+                        const uint32_t o = at[0] + (uint32_t)min(c + i * dc, cols - 1) * 512;
+                        s[i] = lds32f(o);
+                        u[i] = gated ? lds32f(o + 64 * 4) : 0.f;
                     }
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (c + i * dc < cols)
-                        emit(p.e, rc, m0 + c + i * dc, n, s[i], u[i]);
+                    for (int i = 0; i < 8; ++i)
+                        if (c + i * dc < cols)
+                            emit(p.e, rc, m0 + c + i * dc, n, s[i], u[i]);
+                }
+            } else {
+                for (int c = et / rows; c < cols && n < p.e.n; c += 4 * dc) {
+                    float s[4] = {}, u[4] = {};
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (k < split) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t o = at[k] + (uint32_t)min(c + i * dc, cols - 1) * 512;
+                                s[i] += ld_cluster(o);
+                                if (gated)
+                                    u[i] += ld_cluster(o + 64 * 4);
+                            }
+                        }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (c + i * dc < cols)
+                            emit(p.e, rc, m0 + c + i * dc, n, s[i], u[i]);
+                }
             }
         }
-        cluster_sync();  // no CTA leaves while another reads its shared memory
+        if (split == 1)
+            __syncthreads();
+        else
+            cluster_sync();  // no CTA leaves while another reads its shared memory
     } else {
         __syncthreads();
     }
