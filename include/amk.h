@@ -519,9 +519,13 @@ AMK_API int amk_linear(const amk_linear_args *a, void *cuda_stream);
  * window.  Every token sees at least its own row.  Rows that no token sees
  * are never part of a result, whatever they hold (NaN included).
  * All tensors bf16 with contiguous head_dim (1 .. 256); strides in elements.
+ * Cache rows at multiples of 16 bytes with head_dim up to 128 run on the tensor
+ * cores; any others are taken by a slower kernel.
  * k and v have kv_rows >= pos + n_tokens rows per head; the blocks of
  * amk_get_kv have head stride max_ctx * head_dim and row stride head_dim.
- * scale 0 = 1 / sqrt(head_dim).  Softmax statistics and sums are fp32. */
+ * scale 0 = 1 / sqrt(head_dim).  Softmax statistics and sums are fp32, the
+ * weights rounded to bf16 for their product with V.  out overlaps no input.
+ * kv_rows <= 2^30. */
 typedef struct {
     const void *q, *k, *v;            /* [t][h][d], [kv head][row][d] */
     void *out;                        /* [t][h][d] */
@@ -550,7 +554,8 @@ AMK_API int amk_attention(const amk_attention_args *a, void *cuda_stream);
  *  n_accepted: int32 [1].
  * A drafted token outside [0, vocab) is not accepted.  A row that is reached
  * and holds NaN or +inf, or nothing but -inf, has no distribution: nothing is
- * accepted or drawn there (its token is -1).  n_draft <= 64. */
+ * accepted or drawn there (its token is -1).  tokens and n_accepted overlap no
+ * input.  n_draft <= 64, vocab <= 2^30. */
 typedef struct {
     const float *target, *draft, *u;
     const int32_t *draft_tokens;

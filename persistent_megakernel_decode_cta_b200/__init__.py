@@ -7,7 +7,6 @@ There is no CPU fallback: without the built library every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Dict, List, Optional, Tuple
 
@@ -321,8 +320,9 @@ class Decoder:
                            f"outside [0, {self.cfg.max_ctx}) or a token outside [0, {vocab})")
         toks = (abi.c_i32 * max(n, 1))(*tokens)
         if logits is None:
-            with torch.cuda.stream(torch.cuda.ExternalStream(self.stream)) if self.stream else \
-                    contextlib.nullcontext():
+            own = (torch.cuda.ExternalStream(self.stream) if self.stream
+                   else torch.cuda.default_stream())
+            with torch.cuda.stream(own):  # from the pool of the stream that writes it
                 logits = torch.empty((n_logits, vocab), dtype=torch.float32, device="cuda")
         elif logits.dtype is not torch.float32 or logits.shape != (n_logits, vocab) or \
                 not logits.is_contiguous() or not logits.is_cuda:

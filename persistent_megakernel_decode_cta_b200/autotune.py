@@ -59,14 +59,16 @@ def _time_steps(dec: Decoder, ctx: int, steps: int, warmup: int) -> float:
 
 def tune(cfg, weights, ctx: int = 0, kv=None, space: Optional[Dict[str, Iterable[int]]] = None,
          steps: int = 20, warmup: int = 3, token: int = 0,
-         rtol: Optional[float] = None) -> Tuple[object, List[Dict]]:
+         rtol: Optional[float] = None, model: Optional[Dict[str, int]] = None) -> Tuple[object, List[Dict]]:
     """Returns (the fastest passing amk_options, one report row per candidate:
     knobs, status "ok" / "rejected: ..." / "mismatch", us per step, max |dlogit|).
 
     cfg/weights are as for Decoder; kv, if given, is the cache content for
     positions 0..ctx-1 as a [n_layers, 2, n_kv_heads, ctx, head_dim] bf16
-    tensor on the device."""
+    tensor on the device.  model: options that belong to the model, not to the
+    schedule (attn_window, attn_sinks), which every candidate keeps."""
     import torch
+    model = model or {}
 
     if rtol is None:
         # bf16 schedules differ only in rounding order; int8 / int4 GEMVs
@@ -85,15 +87,15 @@ def tune(cfg, weights, ctx: int = 0, kv=None, space: Optional[Dict[str, Iterable
         return dec
 
     logits = torch.empty(cfg.vocab, dtype=torch.float32, device="cuda")
-    ref_dec = make(default_options())
+    ref_dec = make(default_options(**model))
     ref_dec.step(token, ctx, logits=logits)
     ref = logits.clone()
     scale = float(ref.abs().max())
-    best, best_us, rows = default_options(), _time_steps(ref_dec, ctx, steps, warmup), []
+    best, best_us, rows = default_options(**model), _time_steps(ref_dec, ctx, steps, warmup), []
     ref_dec.close()
     rows.append({"knobs": {}, "status": "ok", "us": best_us, "max_dlogit": 0.0})
     for knobs in _candidates(space or DEFAULT_SPACE):
-        opts = default_options(**knobs)
+        opts = default_options(**{**knobs, **model})
         try:
             dec = make(opts)
         except AmkError as e:

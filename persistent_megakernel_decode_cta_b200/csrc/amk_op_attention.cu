@@ -34,6 +34,7 @@ __device__ __forceinline__ void visible(const AttnParams &a, int p, int &s, int 
 // reach the result.  qs: the warp's query in shared memory, pre-scaled, [hd].
 // Writes the elements d for which mine(d).
 constexpr int kMaxHd = 256;
+constexpr int kMaxRows = 1 << 30;  // positions and what is added to them stay in 32 bits
 
 template <typename Mine>
 __device__ void attend_row(const AttnParams &a, int t, int h, const float *qs, Mine mine)
@@ -1003,6 +1004,9 @@ int check_attention(const amk_attention_args *a)
                              a->head_dim, kMaxHd);
     if (a->window < 0 || a->sinks < 0)
         return bad("window or sinks < 0");
+    if (a->kv_rows > kMaxRows)
+        return amk_set_error(AMK_ERR_UNSUPPORTED, "amk_attention: %d rows, at most %d", a->kv_rows,
+                             kMaxRows);
     if (a->pos < 0 || (int64_t)a->pos + a->n_tokens > a->kv_rows)
         return amk_set_error(AMK_ERR_POS_RANGE, "amk_attention: positions %d .. %lld outside the "
                              "%d rows", a->pos, (long long)a->pos + a->n_tokens - 1, a->kv_rows);
@@ -1054,8 +1058,10 @@ extern "C" int amk_attention(const amk_attention_args *a, void *cuda_stream)
     p.group = a->n_heads / a->n_kv_heads;
     p.hd = a->head_dim;
     p.q_pairs = aligned(a->q, 4) && p.q_ts % 2 == 0 && p.q_hs % 2 == 0 && p.hd % 2 == 0;
-    p.window = a->window;
-    p.sinks = a->sinks;
+    // a window or sinks beyond the last row mask nothing more, or less
+    const int n = a->pos + a->n_tokens;
+    p.window = a->window < n ? a->window : 0;
+    p.sinks = a->sinks < n ? a->sinks : n;
     p.scale_log2 = (a->scale > 0.f ? a->scale : 1.f / sqrtf((float)a->head_dim)) * 1.4426950408889634f;
     if (!sm_count())
         return no_device("amk_attention");

@@ -311,6 +311,8 @@ int launch_tc(const amk_linear_args *a, const Epilogue &e, cudaStream_t stream)
     if (!sms)
         return no_device("amk_linear");
     const Choice c = choose(a, sms);
+    if (!c.v.nt)
+        return amk_set_error(AMK_ERR_UNSUPPORTED, "amk_linear: more tiles than a grid holds");
     TcParams p;
     p.e = e;
     const int ksub = a->quant == AMK_QUANT_W4A16 || c.v.split ? 2 : 1;

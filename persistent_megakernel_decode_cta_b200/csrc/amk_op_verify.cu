@@ -21,6 +21,7 @@ namespace {
 constexpr int kThreadsV = 256, kWarps = kThreadsV / 32, kPer = 8;
 constexpr int kChunk = kThreadsV * kPer;
 constexpr int kMaxDraft = 64, kMaxRows = 2 * kMaxDraft + 1;
+constexpr int kMaxVocab = 1 << 30;  // indexes and a chunk beyond them stay in 32 bits
 
 struct RowStat {
     double sum;   // of exp((x - m) / temperature)
@@ -480,6 +481,9 @@ int check_verify(const amk_verify_args *a)
     if (a->n_draft > kMaxDraft)
         return amk_set_error(AMK_ERR_UNSUPPORTED, "amk_verify_draft: %d drafted tokens, at most %d",
                              a->n_draft, kMaxDraft);
+    if (a->vocab > kMaxVocab)
+        return amk_set_error(AMK_ERR_UNSUPPORTED, "amk_verify_draft: vocabulary of %d, at most %d",
+                             a->vocab, kMaxVocab);
     if (!(a->temperature == 0.f || (a->temperature >= 1e-6f && a->temperature <= 1e6f)))
         return bad("temperature is not 0 or within [1e-6, 1e6]");
     if (!a->target || !a->u || !a->tokens || !a->n_accepted || (a->n_draft && !a->draft_tokens))
@@ -501,9 +505,9 @@ int check_verify(const amk_verify_args *a)
 
 extern "C" int64_t amk_verify_workspace(int32_t n_draft, int32_t vocab)
 {
-    if (n_draft < 0 || n_draft > amk::kMaxDraft || vocab < 1)
+    if (n_draft < 0 || n_draft > amk::kMaxDraft || vocab < 1 || vocab > amk::kMaxVocab)
         return amk_set_error(AMK_ERR_INVALID_ARG, "amk_verify_workspace: n_draft outside [0, %d] or "
-                             "vocab < 1", amk::kMaxDraft);
+                             "vocab outside [1, %d]", amk::kMaxDraft, amk::kMaxVocab);
     return amk::workspace_bytes(n_draft, vocab);
 }
 

@@ -224,6 +224,14 @@ def test_attention_masks(window, sinks):
     check_attention(70, 333, 2, 2, 128, window, sinks, seed=window + sinks)
 
 
+@pytest.mark.parametrize("window", [500, 501, 2**30, 2**31 - 2, 2**31 - 1, 2**40])
+@pytest.mark.parametrize("sinks", [0, 2**31 - 1, 2**40])
+def test_attention_masks_beyond_the_last_row(window, sinks):
+    for T, pos, nh, nkv, hd in ((1, 499, 4, 2, 64), (200, 300, 4, 2, 64), (200, 300, 32, 32, 64),
+                                (3, 40, 2, 2, 7)):
+        check_attention(T, pos, nh, nkv, hd, window, sinks, seed=sinks % 7)
+
+
 @pytest.mark.parametrize("T,pos,heads,window,sinks", [
     (1, 20000, (32, 4, 64), 0, 0), (5, 32000, (32, 4, 64), 0, 0), (1, 9000, (32, 32, 128), 0, 0),
     (1, 30000, (9, 3, 64), 4096, 4), (700, 900, (8, 4, 128), 0, 0),
@@ -491,6 +499,56 @@ def test_operators_on_another_stream_and_in_a_graph():
         torch.cuda.synchronize()
         for _, outs in graphs:
             assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_operators_on_two_streams_at_once():
+    """Calls that overlap on the GPU share nothing: each gives what it gives alone."""
+    jobs = []
+    for i in range(2):
+        g = gen(30 + i)
+        x = randn(g, (3, 300)[i], 1024, dtype=BF16)
+        w, s = weights(("int4", "bf16")[i], 700, 1024, i)
+        q = randn(g, (2, 150)[i], 8, 64, dtype=BF16)
+        kv = randn(g, 2, 3000, 64, dtype=BF16)
+        jobs.append((x, w, s, q, kv, draft_case(4, 5000, 40 + i)))
+
+    def run(job, stream=None):
+        x, w, s, q, kv, (target, draft, tok, u) = job
+        return (amk.linear(x, w, scale=s, stream=stream),
+                amk.attention(q, kv, kv, 2500, stream=stream),
+                *amk.verify_draft(target, tok, u, draft_logits=draft, stream=stream))
+
+    want = [run(j) for j in jobs]
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(20):
+        for i in range(2):
+            got[i].append(run(jobs[i], sides[i].cuda_stream))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for outs in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(outs, want[i]))
+
+
+def test_views_of_one_buffer_and_a_leading_batch():
+    """What a model hands over: q as a slice of a joint projection, the result
+    into a slice of a wider buffer."""
+    g = gen(50)
+    n, nh, nkv, hd = 40, 4, 2, 64
+    joint = randn(g, n, (nh + 2 * nkv) * hd, dtype=BF16)
+    q = joint[:, :nh * hd].unflatten(1, (nh, hd))
+    cache = randn(g, 2, nkv, 200, hd, dtype=BF16)
+    wide = torch.zeros(n, 2 * nh * hd, dtype=BF16, device="cuda")
+    out = wide[:, nh * hd:].unflatten(1, (nh, hd))
+    want, tol = oo.attention(q, cache[0], cache[1], 100, 30, 2)
+    assert amk.attention(q, cache[0], cache[1], 100, window=30, sinks=2, out=out) is out
+    close(out, want, tol)
+    assert (wide[:, :nh * hd] == 0).all()
+    w, _ = weights("bf16", 96, nh * hd, 50)
+    y = amk.linear(wide[:, nh * hd:], w, act="silu")
+    want, tol = oo.linear(wide[:, nh * hd:], w, act="silu")
+    close(y, want, tol)
 
 
 def test_no_operator_gave_up_a_wait():

@@ -63,6 +63,7 @@ def test_linear_refuses(kw):
     (dict(window=-1), INVALID), (dict(sinks=-1), INVALID),
     (dict(pos=-1), abi.ERR["AMK_ERR_POS_RANGE"]), (dict(pos=8), abi.ERR["AMK_ERR_POS_RANGE"]),
     (dict(pos=2**31 - 1), abi.ERR["AMK_ERR_POS_RANGE"]),
+    (dict(kv_rows=2**30 + 1), abi.ERR["AMK_ERR_UNSUPPORTED"]),
     (dict(scale=-1.0), INVALID), (dict(scale=float("nan")), INVALID),
     (dict(scale=float("inf")), INVALID), (dict(q=P + 1), INVALID), (dict(out=P + 1), INVALID),
     (dict(out_head_stride=63), INVALID), (dict(out_token_stride=127), INVALID),
@@ -76,7 +77,7 @@ def test_attention_refuses(kw, status):
     (dict(target=None), INVALID), (dict(u=None), INVALID), (dict(tokens=None), INVALID),
     (dict(n_accepted=None), INVALID), (dict(draft_tokens=None), INVALID),
     (dict(n_draft=-1), INVALID), (dict(n_draft=65), abi.ERR["AMK_ERR_UNSUPPORTED"]),
-    (dict(vocab=0), INVALID), (dict(temperature=-1.0), INVALID),
+    (dict(vocab=0), INVALID), (dict(vocab=2**30 + 1), abi.ERR["AMK_ERR_UNSUPPORTED"]), (dict(temperature=-1.0), INVALID),
     (dict(temperature=1e-7), INVALID), (dict(temperature=float("nan")), INVALID),
     (dict(temperature=float("inf")), INVALID), (dict(target_stride=99), INVALID),
     (dict(draft_stride=99), INVALID), (dict(target=P + 2), INVALID), (dict(workspace=None), INVALID),
@@ -88,7 +89,7 @@ def test_verify_refuses(kw, status):
 
 def test_verify_workspace_sizes():
     fn = abi.lib().amk_verify_workspace
-    assert fn(-1, 10) < 0 and fn(65, 10) < 0 and fn(0, 0) < 0
+    assert fn(-1, 10) < 0 and fn(65, 10) < 0 and fn(0, 0) < 0 and fn(0, 2**31 - 1) < 0
     assert 0 < fn(0, 1) <= fn(4, 1) <= fn(4, 128256) < 1 << 20
     assert verify(workspace_bytes=fn(2, 100) - 1) == INVALID
 
