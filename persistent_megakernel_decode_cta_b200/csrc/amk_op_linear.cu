@@ -216,9 +216,9 @@ struct Choice {
     int split, grid;
 };
 
-// What a variant's CTA costs, in us (fitted to some 1160 calls of 60 shapes on
-// B200, 17 .. 2000 tokens; the choices made by it take 1.4 % longer than the
-// fastest variant of each, 22 % at worst): its start and end, each block of 64
+// What a variant's CTA costs, in us (fitted to some 1100 calls of 60 shapes on
+// B200, 17 .. 2000 tokens; the choices made by it take 2 % longer than the
+// fastest variant of each, 23 % at worst): its start and end, each block of 64
 // inputs, each CTA of its cluster, and how much of a block's time a second CTA
 // on the same SM adds.
 struct Cost {
@@ -227,12 +227,12 @@ struct Cost {
 constexpr Cost kSplitCost[3][4] = {  // weight format; 16, 32, 64, 128 tokens
     {{4.9f, 0.20f, 0.12f, 0.28f}, {5.8f, 0.30f, 0.04f, 0.20f},
      {6.5f, 0.31f, 0.10f, 0.27f}, {9.9f, 0.26f, 0.02f, 0.f}},
-    {{4.7f, 0.47f, 0.33f, 0.30f}, {6.7f, 0.37f, 0.65f, 0.f},
-     {8.0f, 0.32f, 0.68f, 0.f}, {10.0f, 0.37f, 0.92f, 0.f}},
-    {{5.2f, 0.32f, 0.23f, 0.54f}, {6.6f, 0.30f, 0.59f, 0.f},
-     {7.3f, 0.32f, 0.61f, 0.f}, {9.4f, 0.39f, 0.81f, 0.f}}};
+    {{4.8f, 0.33f, 0.39f, 0.50f}, {7.0f, 0.32f, 0.59f, 0.f},
+     {8.2f, 0.29f, 0.67f, 0.f}, {10.7f, 0.31f, 0.84f, 0.f}},
+    {{4.7f, 0.30f, 0.35f, 0.45f}, {6.5f, 0.27f, 0.58f, 0.f},
+     {7.5f, 0.27f, 0.68f, 0.f}, {10.0f, 0.34f, 0.88f, 0.f}}};
 constexpr Cost kWalkCost[3][2] = {  // weight format; sums left to the tensor cores, or promoted
-    {{6.1f, 0.36f}, {6.1f, 0.40f}}, {{5.5f, 0.58f}, {6.0f, 0.37f}}, {{6.0f, 0.37f}, {6.0f, 0.37f}}};
+    {{6.1f, 0.36f}, {6.1f, 0.40f}}, {{4.9f, 0.38f}, {5.0f, 0.32f}}, {{3.5f, 0.42f}, {3.5f, 0.42f}}};
 
 Choice choose(const amk_linear_args *a, int sms)
 {
@@ -264,11 +264,14 @@ Choice choose(const amk_linear_args *a, int sms)
         }
     }
     const bool promote = a->y_type == AMK_DT_F32 || a->quant == AMK_QUANT_W4A16;
-    const int nt = codes && promote ? 128 : 256;
+    const int nt = !codes ? 256 : promote ? 128 : 192;
     const int64_t tiles = tn * (((int64_t)a->m + nt - 1) / nt);
     const Cost &c = kWalkCost[a->quant][promote];
+    // a wide tile's gate and up meet after its last sum (40 tokens, int8: 8192 x
+    // 2048 with a gate 21.7 us walking, 16384 x 2048 without 17.7 us)
+    const double gate = a->up ? 4. : 0.;
     consider({nt, false, promote}, 1, tiles, sms,
-             c.fixed + (tiles + sms - 1) / sms * (double)blocks * c.block);
+             c.fixed + gate + (tiles + sms - 1) / sms * (double)blocks * c.block);
     return best;
 }
 
@@ -315,7 +318,7 @@ int launch_tc(const amk_linear_args *a, const Epilogue &e, cudaStream_t stream)
         return amk_set_error(AMK_ERR_UNSUPPORTED, "amk_linear: more tiles than a grid holds");
     TcParams p;
     p.e = e;
-    const int ksub = a->quant == AMK_QUANT_W4A16 || c.v.split ? 2 : 1;
+    const int ksub = a->quant != AMK_QUANT_BF16 || c.v.split ? 2 : 1;
     const int rows = a->up ? 64 : 128;
     p.groups = (a->k + kQ4Group - 1) / kQ4Group;
     p.w_gs = static_cast<const uint16_t *>(a->w_scale);
@@ -341,7 +344,8 @@ int launch_tc(const amk_linear_args *a, const Epilogue &e, cudaStream_t stream)
         else {
             const int per = a->quant == AMK_QUANT_W8A16 ? 1 : 2;  // codes to a byte
             ok = encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, a->k / per, a->n, a->k / per,
-                        ksub * 64 / per, rows, CU_TENSOR_MAP_SWIZZLE_NONE);
+                           ksub * 64 / per, rows,
+                           per == 1 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
         }
     }
     if (!ok)

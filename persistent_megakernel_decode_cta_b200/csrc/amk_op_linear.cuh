@@ -9,12 +9,16 @@
 // token are 32 consecutive outputs.
 //
 // Warps: 0 fetches K blocks with TMA into a ring of stages, 1 issues the MMAs,
-// 2 owns the TMEM, 4.. drain the accumulators (two buffers, so that the next
-// sum runs meanwhile); with int8 and int4 weights four more turn the codes into
-// the bf16 integers they are (exact) in the layout the MMA reads.  int8 row
-// scales are applied to the sums.  The sums of an int4 row's 128-input groups
-// are scaled apart: each group is a sum of its own (`seg`), which the draining
-// warps scale and add in fp32 registers.  So weights are never rounded.
+// 2 owns the TMEM, 4.. drain the accumulators (several buffers, so that the next
+// sum runs meanwhile); with int8 and int4 weights eight more turn the codes into
+// the bf16 integers they are (exact) and write them to TMEM, from where the MMA
+// takes its A: shared memory, which bounds these kernels, then carries the codes
+// and x alone (2048 tokens, 4096 x 11008 int8 gate and up: 390 us with A in
+// shared memory, 325 us so; bf16 weights 266 us).  int8 row scales are applied
+// to the sums.  The sums of an int4 row's 128-input groups are scaled apart: each
+// group is a sum of its own (`seg`), which the draining warps scale and add in
+// fp32 registers, and which costs the time between the two (same call: 596 us).
+// So weights are never rounded.
 //
 // Tensor cores cut off what falls below their accumulators when they align
 // the terms of a sum, always downward in magnitude: over K = 4096 an fp32
@@ -159,15 +163,17 @@ __device__ __forceinline__ uint32_t i4_pair(uint32_t w)
 template <int QUANT, int NT, bool SPLIT, bool PROMOTE>
 struct Cfg {
     // K elements of a stage, in blocks of 64 (one swizzled row of bf16): two
-    // for int4 (rows of 64 bytes) and where the weights only stream through
-    static constexpr int KSUB = QUANT == AMK_QUANT_W4A16 || SPLIT ? 2 : 1;
+    // for codes (one to each of two converting groups) and where the weights
+    // only stream through
+    static constexpr int KSUB = QUANT != AMK_QUANT_BF16 || SPLIT ? 2 : 1;
     static constexpr int BLK = 128 * 128;  // a block of 128 rows of 64 bf16
     static constexpr int A = KSUB * BLK, X = KSUB * NT * 128;
     static constexpr int RAW = QUANT == AMK_QUANT_W8A16   ? KSUB * 64 * 128
                                : QUANT == AMK_QUANT_W4A16 ? KSUB * 32 * 128
                                                           : 0;
     static constexpr int STAGE = X + (RAW ? RAW : A);
-    static constexpr int ASTAGES = !RAW ? 0 : KSUB == 2 ? 2 : 3;  // converted stages
+    static constexpr int ASTAGES = RAW ? 2 : 0;                   // converted stages, in TMEM
+    static constexpr int ACOLS = KSUB * 32;                       // TMEM columns of one
     static constexpr int CW = RAW ? 8 : 0;       // converting warps
     static constexpr int NB = NT <= 64 ? 4 : 2;  // accumulators
     static constexpr int XCH = SPLIT ? 0 : 2 * 2 * 16 * 64 * 4;
@@ -175,19 +181,25 @@ struct Cfg {
     // of an SM's 227 KB: half for a CTA where weights stream (two CTAs to an SM
     // keep the stream going while one starts or ends), else all of it
     static constexpr int ROOM = (CTAS == 2 ? 112 * 1024 : 224 * 1024) - 2048 - XCH;
-    static constexpr int FIT = (ROOM - ASTAGES * A) / STAGE;
+    static constexpr int FIT = ROOM / STAGE;
     static constexpr int STAGES = FIT > 8 ? 8 : FIT;
-    static constexpr int SMEM = STAGES * STAGE + ASTAGES * A + XCH + 1024;
+    static constexpr int SMEM = STAGES * STAGE + XCH + 1024;
     static constexpr int EW = NT >= 64 ? 2 : 1;  // draining warpgroups
     static constexpr int NC = NT / EW;           // columns of each
     static constexpr int THREADS = 128 + EW * 128 + CW * 32;
-    // 640 threads are launched with 96 registers each: 128 x 40 + 256 x 152 +
-    // 256 x 56 of them are no more than that
+    // 640 threads are launched with 96 registers each: 128 x 40 + 256 x 144 +
+    // 256 x 72 of them are no more than that
     static constexpr int REGS = CW && EW == 2 ? 96 : 0;
-    static_assert(!REGS || 128 * 40 + 256 * 152 + 256 * 56 <= THREADS * REGS, "register split");
-    static constexpr int COLS = NB * NT;  // TMEM columns
+    static_assert(!REGS || 128 * 40 + 256 * 144 + 256 * 72 <= THREADS * REGS, "register split");
+    static constexpr int USED = NB * NT + ASTAGES * ACOLS;  // TMEM columns: sums, codes
+    static constexpr int COLS = USED <= 32    ? 32
+                                : USED <= 64  ? 64
+                                : USED <= 128 ? 128
+                                : USED <= 256 ? 256
+                                              : 512;
     static_assert(STAGES >= 2, "a ring needs two stages");
-    static_assert(!SPLIT || NT * 512 <= STAGES * STAGE + ASTAGES * A, "the sums reuse the ring");
+    static_assert(!SPLIT || NT * 512 <= STAGES * STAGE, "the sums reuse the ring");
+    static_assert(NB * NT + ASTAGES * ACOLS <= 512 && CTAS * COLS <= 512, "TMEM columns");
 };
 
 __device__ unsigned int g_timeouts;  // CTAs that gave up a wait
@@ -216,8 +228,7 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
     __shared__ int fail_flag;
     volatile int *fail = &fail_flag;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t abuf = ring + C::STAGES * C::STAGE;  // converted blocks
-    const uint32_t xch = abuf + C::ASTAGES * C::A;
+    const uint32_t xch = ring + C::STAGES * C::STAGE;
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8 * s; };
     auto empty = [&](int s) { return bar0 + 8 * (C::STAGES + s); };
@@ -335,16 +346,21 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
                         }
                         tc_fence_after();
                         const uint32_t xs = ring + s * C::STAGE;
-                        const uint64_t ad = tc_desc(CODES ? abuf + as * C::A : xs + C::X);
-                        const uint64_t bd = tc_desc(xs);
+                        const uint64_t ad = tc_desc(xs + C::X), bd = tc_desc(xs);
+                        const uint32_t at = tmem + C::NB * NT + as * C::ACOLS;
                         if (elect_one()) {
 #pragma unroll
                             for (int j = 0; j < C::KSUB; ++j)
 #pragma unroll
-                                for (int k16 = 0; k16 < 4; ++k16)  // 32 bytes of a row each
-                                    tc_mma(tmem + b * NT, ad + j * (C::BLK >> 4) + 2 * k16,
-                                           bd + j * (NT * 128 >> 4) + 2 * k16, idesc,
-                                           j + k16 ? 1u : accumulate);
+                                for (int k16 = 0; k16 < 4; ++k16) {  // 32 bytes of a row each
+                                    const uint64_t bk = bd + j * (NT * 128 >> 4) + 2 * k16;
+                                    const uint32_t add = j + k16 ? 1u : accumulate;
+                                    if (CODES)
+                                        tc_mma_ta(tmem + b * NT, at + j * 32 + k16 * 8, bk, idesc, add);
+                                    else
+                                        tc_mma(tmem + b * NT, ad + j * (C::BLK >> 4) + 2 * k16, bk,
+                                               idesc, add);
+                                }
                             if (CODES)
                                 tc_commit(aempty(as));
                             tc_commit(empty(s));
@@ -367,7 +383,7 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
         }
     } else if (warp < 4 + 4 * C::EW) {
         if constexpr (C::REGS != 0)
-            setmaxnreg_inc<152>();
+            setmaxnreg_inc<144>();
         const int wg = (warp - 4) >> 2, q = warp & 3, r = q * 32 + lane;  // row of the tile
         const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + wg * C::NC;
         uint32_t sc = 0;
@@ -502,8 +518,10 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
         }
     } else if constexpr (CODES) {
         if constexpr (C::REGS != 0)
-            setmaxnreg_dec<56>();
-        const int cw = warp - 4 - 4 * C::EW;  // converts rows 16 cw .. 16 cw + 15
+            setmaxnreg_dec<72>();
+        // the warps of a group take 32 rows each of its block of a stage
+        const int j = (warp - 4 - 4 * C::EW) >> 2;
+        const int row = (warp & 3) * 32 + lane;
         uint32_t ph = 0, aph = 1;
         int s = 0, as = 0;
         bool ok = true;
@@ -514,50 +532,44 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
                     break;
                 }
                 const uint32_t src = ring + s * C::STAGE + C::X;
-                constexpr int NV = C::RAW / (C::CW * 512);  // 16-byte pieces of a lane
+                // a lane takes a row's 64 codes of block j: 16-byte pieces that lie
+                // swizzled by row, so that eight lanes' loads share no bank
+                constexpr int NV = QUANT == AMK_QUANT_W8A16 ? 4 : 2;
+                constexpr int PITCH = C::RAW / 128;
+                const int sw = QUANT == AMK_QUANT_W8A16 ? row & 7 : (row >> 1) & 3;
                 uint4 v[NV];
 #pragma unroll
-                for (int i = 0; i < NV; ++i)  // the warp's 16 rows of codes, in order
-                    v[i] = lds128(src + cw * (C::RAW / C::CW) + i * 512 + lane * 16);
+                for (int i = 0; i < NV; ++i) {
+                    const int piece = j * NV + i;
+                    v[i] = lds128(src + row * PITCH + ((piece ^ sw) << 4));
+                }
+                uint32_t o[32];
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (QUANT == AMK_QUANT_W8A16) {
+                            o[i * 8 + 2 * e] = i8_pair(__byte_perm(w[e], 0, 0x4140));
+                            o[i * 8 + 2 * e + 1] = i8_pair(__byte_perm(w[e], 0, 0x4342));
+                        } else {
+                            const uint32_t lo = w[e], hi = lo >> 4;
+                            o[i * 16 + 4 * e] = i4_pair(__byte_perm(lo, hi, 0x0400));
+                            o[i * 16 + 4 * e + 1] = i4_pair(__byte_perm(lo, hi, 0x0501));
+                            o[i * 16 + 4 * e + 2] = i4_pair(__byte_perm(lo, hi, 0x0602));
+                            o[i * 16 + 4 * e + 3] = i4_pair(__byte_perm(lo, hi, 0x0703));
+                        }
+                    }
+                }
                 if (!warp_wait(aempty(as), aph, fail)) {
                     ok = false;
                     break;
                 }
-                const uint32_t dst = abuf + as * C::A;
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                    if (QUANT == AMK_QUANT_W8A16) {
-                        // a piece is 16 codes; KSUB * 4 of them make a row
-                        const int at = i * 32 + lane;
-                        const int row = cw * 16 + at / (C::KSUB * 4), pc = at % (C::KSUB * 4);
-                        const uint32_t d = dst + (pc >> 2) * C::BLK + row * 128;
-                        const int c = 2 * (pc & 3);
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            sts128(d + (((c + e) ^ (row & 7)) << 4),
-                                   i8_pair(__byte_perm(w[2 * e], 0, 0x4140)),
-                                   i8_pair(__byte_perm(w[2 * e], 0, 0x4342)),
-                                   i8_pair(__byte_perm(w[2 * e + 1], 0, 0x4140)),
-                                   i8_pair(__byte_perm(w[2 * e + 1], 0, 0x4342)));
-                    } else {
-                        // a piece is 32 codes; KSUB * 2 of them make a row
-                        const int at = i * 32 + lane;
-                        const int row = cw * 16 + at / (C::KSUB * 2), pc = at % (C::KSUB * 2);
-                        const uint32_t d = dst + (pc >> 1) * C::BLK + row * 128;
-                        const int c = 4 * (pc & 1);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t lo = w[e], hi = lo >> 4;
-                            sts128(d + (((c + e) ^ (row & 7)) << 4),
-                                   i4_pair(__byte_perm(lo, hi, 0x0400)),
-                                   i4_pair(__byte_perm(lo, hi, 0x0501)),
-                                   i4_pair(__byte_perm(lo, hi, 0x0602)),
-                                   i4_pair(__byte_perm(lo, hi, 0x0703)));
-                        }
-                    }
-                }
-                fence_async_smem();
+                tc_fence_after();
+                tmem_st32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::NB * NT + as * C::ACOLS +
+                              j * 32, o);
+                tmem_st_wait();
+                tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(afull(as));
@@ -681,12 +693,14 @@ cudaError_t launch_variant(const Variant &v, const TcParams &p, int grid, cudaSt
         default: return launch_one<QUANT, 128, true, true>(p, grid, stream);
         }
     // eight draining warps hold 256 columns of 128 sums in registers; beside
-    // four converting warps there is room for half of them
+    // the converting warps there is room for half of them.  Two buffers of 192
+    // columns and the codes fill the TMEM
     constexpr int WIDE = QUANT == AMK_QUANT_BF16 ? 256 : 128;
     if (v.promote || QUANT == AMK_QUANT_W4A16)
         return launch_one<QUANT, WIDE, false, true>(p, grid, stream);
     if constexpr (QUANT != AMK_QUANT_W4A16)
-        return launch_one<QUANT, 256, false, false>(p, grid, stream);
+        return launch_one<QUANT, QUANT == AMK_QUANT_BF16 ? 256 : 192, false, false>(p, grid,
+                                                                                    stream);
     return cudaErrorInvalidValue;
 }
 
