@@ -771,7 +771,9 @@ __global__ void __launch_bounds__(TcCfg<HD>::THREADS, 2)
 #pragma unroll
             for (int c = 0; c < kKeys; c += 16)
                 tmem_ld16(tmem + lanes + b * kKeys + c, *reinterpret_cast<float(*)[16]>(s + c));
-            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < kKeys; c += 16)
+                tmem_ld_wait(*reinterpret_cast<float(*)[16]>(s + c));
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
@@ -813,7 +815,7 @@ __global__ void __launch_bounds__(TcCfg<HD>::THREADS, 2)
                 for (int c = 0; c < HD; c += 16) {
                     float o[16];
                     tmem_ld16(tmem + lanes + 128 + c, o);
-                    tmem_ld_wait();
+                    tmem_ld_wait(o);
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
                         o[e] *= corr;
@@ -848,7 +850,7 @@ __global__ void __launch_bounds__(TcCfg<HD>::THREADS, 2)
                 float o[16] = {};
                 if (tn > 0) {
                     tmem_ld16(tmem + lanes + 128 + c, o);
-                    tmem_ld_wait();
+                    tmem_ld_wait(o);
                 }
 #pragma unroll
                 for (int e = 0; e < 16; e += 4)
@@ -864,7 +866,7 @@ __global__ void __launch_bounds__(TcCfg<HD>::THREADS, 2)
             for (int c = 0; c < HD; c += 16) {
                 float o[16];
                 tmem_ld16(tmem + lanes + 128 + c, o);
-                tmem_ld_wait();
+                tmem_ld_wait(o);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     o[e] *= inv;

@@ -218,7 +218,7 @@ struct Choice {
 
 // What a variant's CTA costs, in us (fitted to some 1100 calls of 60 shapes on
 // B200, 17 .. 2000 tokens; the choices made by it take 2 % longer than the
-// fastest variant of each, 23 % at worst): its start and end, each block of 64
+// fastest variant of each, 18 % at worst): its start and end, each block of 64
 // inputs, each CTA of its cluster, and how much of a block's time a second CTA
 // on the same SM adds.
 struct Cost {
@@ -227,12 +227,12 @@ struct Cost {
 constexpr Cost kSplitCost[3][4] = {  // weight format; 16, 32, 64, 128 tokens
     {{4.9f, 0.20f, 0.12f, 0.28f}, {5.8f, 0.30f, 0.04f, 0.20f},
      {6.5f, 0.31f, 0.10f, 0.27f}, {9.9f, 0.26f, 0.02f, 0.f}},
-    {{4.8f, 0.33f, 0.39f, 0.50f}, {7.0f, 0.32f, 0.59f, 0.f},
-     {8.2f, 0.29f, 0.67f, 0.f}, {10.7f, 0.31f, 0.84f, 0.f}},
-    {{4.7f, 0.30f, 0.35f, 0.45f}, {6.5f, 0.27f, 0.58f, 0.f},
-     {7.5f, 0.27f, 0.68f, 0.f}, {10.0f, 0.34f, 0.88f, 0.f}}};
+    {{4.9f, 0.28f, 0.39f, 0.58f}, {7.3f, 0.24f, 0.56f, 0.f},
+     {8.4f, 0.25f, 0.66f, 0.f}, {10.8f, 0.29f, 0.88f, 0.f}},
+    {{4.8f, 0.24f, 0.36f, 0.60f}, {6.8f, 0.23f, 0.56f, 0.f},
+     {7.8f, 0.26f, 0.65f, 0.f}, {10.2f, 0.33f, 0.85f, 0.f}}};
 constexpr Cost kWalkCost[3][2] = {  // weight format; sums left to the tensor cores, or promoted
-    {{6.1f, 0.36f}, {6.1f, 0.40f}}, {{4.9f, 0.38f}, {5.0f, 0.32f}}, {{3.5f, 0.42f}, {3.5f, 0.42f}}};
+    {{6.1f, 0.36f}, {6.1f, 0.40f}}, {{5.2f, 0.39f}, {5.4f, 0.30f}}, {{4.0f, 0.37f}, {4.0f, 0.37f}}};
 
 Choice choose(const amk_linear_args *a, int sms)
 {
@@ -268,7 +268,7 @@ Choice choose(const amk_linear_args *a, int sms)
     const int64_t tiles = tn * (((int64_t)a->m + nt - 1) / nt);
     const Cost &c = kWalkCost[a->quant][promote];
     // a wide tile's gate and up meet after its last sum (40 tokens, int8: 8192 x
-    // 2048 with a gate 21.7 us walking, 16384 x 2048 without 17.7 us)
+    // 2048 with a gate 21.7 us walking, 16384 x 2048 without 18.3 us)
     const double gate = a->up ? 4. : 0.;
     consider({nt, false, promote}, 1, tiles, sms,
              c.fixed + gate + (tiles + sms - 1) / sms * (double)blocks * c.block);

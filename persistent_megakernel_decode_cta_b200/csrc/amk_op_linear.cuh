@@ -14,10 +14,10 @@
 // the bf16 integers they are (exact) and write them to TMEM, from where the MMA
 // takes its A: shared memory, which bounds these kernels, then carries the codes
 // and x alone (2048 tokens, 4096 x 11008 int8 gate and up: 390 us with A in
-// shared memory, 325 us so; bf16 weights 266 us).  int8 row scales are applied
+// shared memory, 330 us so; bf16 weights 266 us).  int8 row scales are applied
 // to the sums.  The sums of an int4 row's 128-input groups are scaled apart: each
 // group is a sum of its own (`seg`), which the draining warps scale and add in
-// fp32 registers, and which costs the time between the two (same call: 596 us).
+// fp32 registers, and which costs the time between the two (same call: 538 us).
 // So weights are never rounded.
 //
 // Tensor cores cut off what falls below their accumulators when they align
@@ -175,7 +175,7 @@ struct Cfg {
     static constexpr int ASTAGES = RAW ? 2 : 0;                   // converted stages, in TMEM
     static constexpr int ACOLS = KSUB * 32;                       // TMEM columns of one
     static constexpr int CW = RAW ? 8 : 0;       // converting warps
-    static constexpr int NB = NT <= 64 ? 4 : 2;  // accumulators
+    static constexpr int NB = NT <= 64 ? 4 : RAW && NT == 128 ? 3 : 2;  // accumulators
     static constexpr int XCH = SPLIT ? 0 : 2 * 2 * 16 * 64 * 4;
     static constexpr int CTAS = SPLIT && NT <= (RAW ? 16 : 64) ? 2 : 1;  // to an SM
     // of an SM's 227 KB: half for a CTA where weights stream (two CTAs to an SM
@@ -187,10 +187,11 @@ struct Cfg {
     static constexpr int EW = NT >= 64 ? 2 : 1;  // draining warpgroups
     static constexpr int NC = NT / EW;           // columns of each
     static constexpr int THREADS = 128 + EW * 128 + CW * 32;
-    // 640 threads are launched with 96 registers each: 128 x 40 + 256 x 144 +
-    // 256 x 72 of them are no more than that
+    // 640 threads are launched with 96 registers each: 128 x 40 + 256 x DRAIN +
+    // 256 x CONVERT of them are no more than that
     static constexpr int REGS = CW && EW == 2 ? 96 : 0;
-    static_assert(!REGS || 128 * 40 + 256 * 144 + 256 * 72 <= THREADS * REGS, "register split");
+    static constexpr int DRAIN = 136, CONVERT = 80;
+    static_assert(!REGS || 128 * 40 + 256 * (DRAIN + CONVERT) <= THREADS * REGS, "register split");
     static constexpr int USED = NB * NT + ASTAGES * ACOLS;  // TMEM columns: sums, codes
     static constexpr int COLS = USED <= 32    ? 32
                                 : USED <= 64  ? 64
@@ -204,15 +205,14 @@ struct Cfg {
 
 __device__ unsigned int g_timeouts;  // CTAs that gave up a wait
 
-template <int N>
-__device__ __forceinline__ void setmaxnreg_inc()
+// A warpgroup's registers from FROM, with which it was launched, to TO a thread.
+template <int FROM, int TO>
+__device__ __forceinline__ void setmaxnreg_to()
 {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void setmaxnreg_dec()
-{
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+    if constexpr (TO > FROM)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(TO));
+    else
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TO));
 }
 
 template <int QUANT, int NT, bool SPLIT, bool PROMOTE>
@@ -241,10 +241,10 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
         fail_flag = 0;
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(full(s), 1);
-            mbar_init(empty(s), 1 + C::CW);  // the MMAs, and the converting warps
+            mbar_init(empty(s), 1 + C::CW / 2);  // the MMAs, and the stage's converting warps
         }
         for (int s = 0; s < C::ASTAGES; ++s) {
-            mbar_init(afull(s), C::CW);
+            mbar_init(afull(s), C::CW / 2);
             mbar_init(aempty(s), 1);
         }
         for (int b = 0; b < C::NB; ++b) {
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
     // registers that the others give up
     if (warp < 4) {
         if constexpr (C::REGS != 0)
-            setmaxnreg_dec<40>();
+            setmaxnreg_to<C::REGS, 40>();
         if (warp == 0) {
             uint32_t it = 0, ph = 1;
             int s = 0;
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
         }
     } else if (warp < 4 + 4 * C::EW) {
         if constexpr (C::REGS != 0)
-            setmaxnreg_inc<144>();
+            setmaxnreg_to<C::REGS, C::DRAIN>();
         const int wg = (warp - 4) >> 2, q = warp & 3, r = q * 32 + lane;  // row of the tile
         const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + wg * C::NC;
         uint32_t sc = 0;
@@ -414,16 +414,19 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
                         break;
                     }
                     tc_fence_after();
+                    float v[2][16];
+                    tmem_ld16(taddr + b * NT, v[0]);
 #pragma unroll
                     for (int c0 = 0; c0 < C::NC; c0 += 16) {
-                        float v[16];
-                        tmem_ld16(taddr + b * NT + c0, v);
-                        tmem_ld_wait();
+                        float(&w)[16] = v[(c0 >> 4) & 1];
+                        tmem_ld_wait(w);
+                        if (c0 + 16 < C::NC)  // the next columns come meanwhile
+                            tmem_ld16(taddr + b * NT + c0 + 16, v[(c0 >> 4) & 1 ^ 1]);
 #pragma unroll
                         for (int c = 0; c < 16; ++c)
                             acc[c0 + c] = QUANT == AMK_QUANT_W4A16
-                                              ? fmaf(v[c], scale, acc[c0 + c])
-                                              : acc[c0 + c] + v[c];
+                                              ? fmaf(w[c], scale, acc[c0 + c])
+                                              : acc[c0 + c] + w[c];
                     }
                     if (!SPLIT && kb + p.seg >= kb1) {
                         // the tile's sums go back into the last buffer, from where
@@ -475,7 +478,7 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
                     float res[16];
                     if (p.e.residual)
                         residual16(p.e, mc, n, nc, res);
-                    tmem_ld_wait();
+                    tmem_ld_wait(v);
                     if (!is_up) {
 #pragma unroll
                         for (int c = 0; c < 16; ++c)
@@ -518,65 +521,66 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
         }
     } else if constexpr (CODES) {
         if constexpr (C::REGS != 0)
-            setmaxnreg_dec<72>();
-        // the warps of a group take 32 rows each of its block of a stage
-        const int j = (warp - 4 - 4 * C::EW) >> 2;
-        const int row = (warp & 3) * 32 + lane;
-        uint32_t ph = 0, aph = 1;
-        int s = 0, as = 0;
+            setmaxnreg_to<C::REGS, C::CONVERT>();
+        // the two groups of four warps take the stages by turns, a warp 32 rows
+        const int grp = (warp - 4 - 4 * C::EW) >> 2, row = (warp & 3) * 32 + lane;
+        static_assert(C::ASTAGES == 2 && C::CW == 8 && C::KSUB == 2, "a group to a stage");
+        const uint32_t dst =
+            tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::NB * NT + grp * C::ACOLS;
+        uint32_t it = 0, ph = 0, aph = 1;
+        int s = 0;
         bool ok = true;
         for (int tile = first; tile < p.tiles && ok; tile += step)
-            for (int kb = kb0; kb < kb1 && ok; ++kb) {
-                if (!warp_wait(full(s), ph, fail)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t src = ring + s * C::STAGE + C::X;
-                // a lane takes a row's 64 codes of block j: 16-byte pieces that lie
-                // swizzled by row, so that eight lanes' loads share no bank
-                constexpr int NV = QUANT == AMK_QUANT_W8A16 ? 4 : 2;
-                constexpr int PITCH = C::RAW / 128;
-                const int sw = QUANT == AMK_QUANT_W8A16 ? row & 7 : (row >> 1) & 3;
-                uint4 v[NV];
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int piece = j * NV + i;
-                    v[i] = lds128(src + row * PITCH + ((piece ^ sw) << 4));
-                }
-                uint32_t o[32];
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (QUANT == AMK_QUANT_W8A16) {
-                            o[i * 8 + 2 * e] = i8_pair(__byte_perm(w[e], 0, 0x4140));
-                            o[i * 8 + 2 * e + 1] = i8_pair(__byte_perm(w[e], 0, 0x4342));
-                        } else {
-                            const uint32_t lo = w[e], hi = lo >> 4;
-                            o[i * 16 + 4 * e] = i4_pair(__byte_perm(lo, hi, 0x0400));
-                            o[i * 16 + 4 * e + 1] = i4_pair(__byte_perm(lo, hi, 0x0501));
-                            o[i * 16 + 4 * e + 2] = i4_pair(__byte_perm(lo, hi, 0x0602));
-                            o[i * 16 + 4 * e + 3] = i4_pair(__byte_perm(lo, hi, 0x0703));
-                        }
+            for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
+                if ((it & 1) == grp) {
+                    if (!warp_wait(full(s), ph, fail)) {
+                        ok = false;
+                        break;
                     }
-                }
-                if (!warp_wait(aempty(as), aph, fail)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                tmem_st32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::NB * NT + as * C::ACOLS +
-                              j * 32, o);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(afull(as));
-                    mbar_arrive(empty(s));
-                }
-                if (++as == C::ASTAGES) {
-                    as = 0;
+                    const uint32_t src = ring + s * C::STAGE + C::X;
+                    // a lane takes a row's 128 codes: 16-byte pieces that lie swizzled
+                    // by row, so that eight lanes' loads share no bank
+                    constexpr int NV = C::RAW / 2048, PITCH = C::RAW / 128;
+                    const int sw = QUANT == AMK_QUANT_W8A16 ? row & 7 : (row >> 1) & 3;
+                    // (both blocks before the wait took 2 % longer)
+#pragma unroll
+                    for (int j = 0; j < C::KSUB; ++j) {
+                        uint32_t o[32];
+#pragma unroll
+                        for (int i = 0; i < NV / 2; ++i) {
+                            const int piece = j * NV / 2 + i;
+                            const uint4 v = lds128(src + row * PITCH + ((piece ^ sw) << 4));
+                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                            uint32_t *d = o + i * (64 / NV);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                if (QUANT == AMK_QUANT_W8A16) {
+                                    d[2 * e] = i8_pair(__byte_perm(w[e], 0, 0x4140));
+                                    d[2 * e + 1] = i8_pair(__byte_perm(w[e], 0, 0x4342));
+                                } else {
+                                    const uint32_t lo = w[e], hi = lo >> 4;
+                                    d[4 * e] = i4_pair(__byte_perm(lo, hi, 0x0400));
+                                    d[4 * e + 1] = i4_pair(__byte_perm(lo, hi, 0x0501));
+                                    d[4 * e + 2] = i4_pair(__byte_perm(lo, hi, 0x0602));
+                                    d[4 * e + 3] = i4_pair(__byte_perm(lo, hi, 0x0703));
+                                }
+                            }
+                        }
+                        if (j == 0) {
+                            ok = warp_wait(aempty(grp), aph, fail);
+                            tc_fence_after();
+                        }
+                        tmem_st32(dst + j * 32, o);
+                    }
+                    if (!ok)
+                        break;
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(afull(grp));
+                        mbar_arrive(empty(s));
+                    }
                     aph ^= 1;
                 }
                 if (++s == C::STAGES) {
