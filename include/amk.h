@@ -329,7 +329,7 @@ AMK_API int amk_decode_step_host(amk_handle *h, int32_t token_id, int32_t pos,
  *  tokens: host int32 [n], read before the call returns.
  * By matrix products over several tokens (amk_linear, amk_attention below), not
  * the persistent kernel: their inputs are rounded to bf16 (the single-token
- * step's to 15 bits or none), so logits differ from a step's by about 2^-9 of
+ * step's to 15 bits or none), so logits differ from a step's by about 2^-8 of
  * their size.  Asynchronous on the handle's stream, which must not be capturing
  * (AMK_ERR_UNSUPPORTED).  The first call allocates the activations.  A step
  * that follows with token_id -1 is refused (this call chooses no token: see

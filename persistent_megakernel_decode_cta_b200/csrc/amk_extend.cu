@@ -60,6 +60,39 @@ __global__ void __launch_bounds__(256) norm_rows(float *x, const uint16_t *embed
     float *xr = x + (int64_t)t * hidden;
     const uint16_t *er = EMBED ? embed + (int64_t)tokens[t] * hidden : nullptr;
     float s = 0.f;
+    if (!EMBED && hidden % 4 == 0 && hidden <= 4096 && ((uintptr_t)gain & 7) == 0) {
+        // a row in registers: one latency for its loads
+        const int quads = hidden / 4;
+        float4 v[4];
+        uint2 gn[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = threadIdx.x + j * 256;
+            v[j] = i < quads ? reinterpret_cast<const float4 *>(xr)[i] : make_float4(0, 0, 0, 0);
+            gn[j] = i < quads ? reinterpret_cast<const uint2 *>(gain)[i] : make_uint2(0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            s = fmaf(v[j].x, v[j].x, s);
+            s = fmaf(v[j].y, v[j].y, s);
+            s = fmaf(v[j].z, v[j].z, s);
+            s = fmaf(v[j].w, v[j].w, s);
+        }
+        const float r = rsqrtf(block_sum(s) / (float)hidden + eps);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = threadIdx.x + j * 256;
+            if (i < quads) {
+                uint2 o;
+                o.x = f_bf16(v[j].x * r * bf16f((uint16_t)gn[j].x)) |
+                      (uint32_t)f_bf16(v[j].y * r * bf16f((uint16_t)(gn[j].x >> 16))) << 16;
+                o.y = f_bf16(v[j].z * r * bf16f((uint16_t)gn[j].y)) |
+                      (uint32_t)f_bf16(v[j].w * r * bf16f((uint16_t)(gn[j].y >> 16))) << 16;
+                reinterpret_cast<uint2 *>(xn + (int64_t)t * hidden)[i] = o;
+            }
+        }
+        return;
+    }
     for (int i = threadIdx.x; i < hidden; i += 256) {
         float v;
         if (EMBED) {
@@ -76,29 +109,31 @@ __global__ void __launch_bounds__(256) norm_rows(float *x, const uint16_t *embed
 }
 
 // Rotates q and k (pairs i, i + hd / 2), and writes q, and k and v into the
-// cache rows pos + t: one token to a CTA.
+// cache rows pos + t: a thread to a pair of a token, so that each has one
+// latency; parts CTAs to a token.
 __global__ void __launch_bounds__(256) rope_append(const float *qkv, const float2 *rope,
                                                    uint16_t *q, uint16_t *kc, uint16_t *vc, int nh,
-                                                   int nkv, int hd, int pos, int max_ctx)
+                                                   int nkv, int hd, int pos, int max_ctx,
+                                                   int parts)
 {
     pdl_wait();
     pdl_launch();
-    const int t = blockIdx.x, half = hd / 2;
+    const int t = blockIdx.x / parts, half = hd / 2;
+    const int i = blockIdx.x % parts * 256 + threadIdx.x;
     const float *src = qkv + (int64_t)t * (nh + 2 * nkv) * hd;
     const float2 *cs = rope + (int64_t)t * half;
-    for (int i = threadIdx.x; i < (nh + nkv) * half; i += 256) {
-        const int h = i / half, e = i - h * half;
+    const int h = i / half, e = i - h * half;
+    if (h < nh + nkv) {
         const float a = src[h * hd + e], b = src[h * hd + e + half];
         const float2 r = cs[e];
         uint16_t *dst = h < nh ? q + ((int64_t)t * nh + h) * hd
                                : kc + ((int64_t)(h - nh) * max_ctx + pos + t) * hd;
         dst[e] = f_bf16(a * r.x - b * r.y);
         dst[e + half] = f_bf16(b * r.x + a * r.y);
-    }
-    const float *v = src + (nh + nkv) * hd;
-    for (int i = threadIdx.x; i < nkv * hd; i += 256) {
-        const int h = i / hd;
-        vc[((int64_t)h * max_ctx + pos + t) * hd + (i - h * hd)] = f_bf16(v[i]);
+    } else if (h < nh + 2 * nkv) {
+        uint16_t *dst = vc + ((int64_t)(h - nh - nkv) * max_ctx + pos + t) * hd;
+        dst[e] = f_bf16(src[h * hd + e]);
+        dst[e + half] = f_bf16(src[h * hd + e + half]);
     }
 }
 
@@ -158,7 +193,7 @@ int extend_chunk(const amk_config &c, const ModelWeights &w, const ExtendBuffers
                  float *logits, cudaStream_t stream)
 {
     const int hd = c.head_dim, half = hd / 2, qo = c.n_heads * hd, ko = c.n_kv_heads * hd;
-    const int qkv = qo + 2 * ko;
+    const int qkv = qo + 2 * ko, parts = (qkv / 2 + 255) / 256;
     const size_t block = (size_t)c.n_kv_heads * c.max_ctx * hd;  // K or V of a layer
     auto gain = [](const void *p) { return static_cast<const uint16_t *>(p); };
     auto linear = [&](const uint16_t *x, int k, const void *mat, const void *scale, int out,
@@ -190,8 +225,8 @@ int extend_chunk(const amk_config &c, const ModelWeights &w, const ExtendBuffers
             (rc = linear(b.xn, c.hidden, w.mat[W_K][l], sc(W_K, l), ko, b.qkv + qo, qkv, nullptr)) ||
             (rc = linear(b.xn, c.hidden, w.mat[W_V][l], sc(W_V, l), ko, b.qkv + qo + ko, qkv,
                          nullptr)) ||
-            (rc = launch(rope_append, n, stream, b.qkv, b.rope, b.q, kc, vc, c.n_heads,
-                         c.n_kv_heads, hd, pos, c.max_ctx)))
+            (rc = launch(rope_append, n * parts, stream, b.qkv, b.rope, b.q, kc, vc, c.n_heads,
+                         c.n_kv_heads, hd, pos, c.max_ctx, parts)))
             break;
         amk_attention_args a{};
         a.q = b.q;

@@ -218,7 +218,7 @@ struct Choice {
 
 // What a variant's CTA costs, in us (fitted to some 1100 calls of 60 shapes on
 // B200, 17 .. 2000 tokens; the choices made by it take 2 % longer than the
-// fastest variant of each, 18 % at worst): its start and end, each block of 64
+// fastest variant of each, 26 % at worst): its start and end, each block of 64
 // inputs, each CTA of its cluster, and how much of a block's time a second CTA
 // on the same SM adds.
 struct Cost {
@@ -227,12 +227,12 @@ struct Cost {
 constexpr Cost kSplitCost[3][4] = {  // weight format; 16, 32, 64, 128 tokens
     {{4.9f, 0.20f, 0.12f, 0.28f}, {5.8f, 0.30f, 0.04f, 0.20f},
      {6.5f, 0.31f, 0.10f, 0.27f}, {9.9f, 0.26f, 0.02f, 0.f}},
-    {{4.9f, 0.28f, 0.39f, 0.58f}, {7.3f, 0.24f, 0.56f, 0.f},
-     {8.4f, 0.25f, 0.66f, 0.f}, {10.8f, 0.29f, 0.88f, 0.f}},
-    {{4.8f, 0.24f, 0.36f, 0.60f}, {6.8f, 0.23f, 0.56f, 0.f},
-     {7.8f, 0.26f, 0.65f, 0.f}, {10.2f, 0.33f, 0.85f, 0.f}}};
+    {{5.3f, 0.21f, 0.32f, 0.62f}, {7.4f, 0.19f, 0.50f, 0.f},
+     {8.6f, 0.20f, 0.59f, 0.f}, {10.5f, 0.26f, 0.87f, 0.f}},
+    {{5.0f, 0.23f, 0.30f, 0.52f}, {6.9f, 0.22f, 0.50f, 0.f},
+     {8.0f, 0.25f, 0.61f, 0.f}, {10.3f, 0.31f, 0.80f, 0.f}}};
 constexpr Cost kWalkCost[3][2] = {  // weight format; sums left to the tensor cores, or promoted
-    {{6.1f, 0.36f}, {6.1f, 0.40f}}, {{5.2f, 0.39f}, {5.4f, 0.30f}}, {{4.0f, 0.37f}, {4.0f, 0.37f}}};
+    {{6.1f, 0.36f}, {6.1f, 0.40f}}, {{5.4f, 0.36f}, {4.9f, 0.27f}}, {{3.8f, 0.36f}, {3.8f, 0.36f}}};
 
 Choice choose(const amk_linear_args *a, int sms)
 {
@@ -263,15 +263,17 @@ Choice choose(const amk_linear_args *a, int sms)
                      waves * (c.fixed + (blocks + split - 1) / split * block) + split * c.member);
         }
     }
-    const bool promote = a->y_type == AMK_DT_F32 || a->quant == AMK_QUANT_W4A16;
-    const int nt = !codes ? 256 : promote ? 128 : 192;
-    const int64_t tiles = tn * (((int64_t)a->m + nt - 1) / nt);
-    const Cost &c = kWalkCost[a->quant][promote];
     // a wide tile's gate and up meet after its last sum (40 tokens, int8: 8192 x
     // 2048 with a gate 21.7 us walking, 16384 x 2048 without 18.3 us)
     const double gate = a->up ? 4. : 0.;
-    consider({nt, false, promote}, 1, tiles, sms,
-             c.fixed + gate + (tiles + sms - 1) / sms * (double)blocks * c.block);
+    const bool must = a->y_type == AMK_DT_F32 || a->quant == AMK_QUANT_W4A16;
+    for (int promote = must; promote <= (must || codes); ++promote) {
+        const int nt = !codes ? 256 : promote ? 128 : 192;
+        const int64_t tiles = tn * (((int64_t)a->m + nt - 1) / nt);
+        const Cost &c = kWalkCost[a->quant][promote];
+        consider({nt, false, promote != 0}, 1, tiles, sms,
+                 c.fixed + gate + (tiles + sms - 1) / sms * (double)blocks * c.block);
+    }
     return best;
 }
 

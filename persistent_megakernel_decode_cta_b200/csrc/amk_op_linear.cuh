@@ -17,7 +17,7 @@
 // shared memory, 330 us so; bf16 weights 266 us).  int8 row scales are applied
 // to the sums.  The sums of an int4 row's 128-input groups are scaled apart: each
 // group is a sum of its own (`seg`), which the draining warps scale and add in
-// fp32 registers, and which costs the time between the two (same call: 538 us).
+// fp32 registers, and which costs the time between the two (same call: 520 us).
 // So weights are never rounded.
 //
 // Tensor cores cut off what falls below their accumulators when they align
@@ -142,22 +142,30 @@ __device__ __forceinline__ void emit(const Epilogue &e, const RowConst &c, int m
 }
 
 // Exact bf16 pairs of int8 codes: 128 + the low seven bits, less 256 or 128 by
-// the sign.  w holds the codes in the low bytes of its halves.
-__device__ __forceinline__ uint32_t i8_pair(uint32_t w)
+// the sign.  The bytes of w that sel picks, 0x4140 or 0x4342, are the mantissas
+// under an exponent of 0x43, whose last bit is then the sign.
+__device__ __forceinline__ uint32_t i8_pair(uint32_t w, uint32_t sel)
 {
-    const uint32_t a = (w & 0x007f007fu) | 0x43004300u, s = (w & 0x00800080u) | 0x43004300u;
+    const uint32_t b = __byte_perm(w, 0x43434343u, sel);
+    const uint32_t a = b & 0xff7fff7fu, s = b & 0xff80ff80u;
     uint32_t r;
     asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(s));
     return r;
 }
-// Exact bf16 pairs of int4 codes in the low nibbles of the halves: 128 + (code
-// + 8), less 136.
-__device__ __forceinline__ uint32_t i4_pair(uint32_t w)
+// Exact bf16 pairs of a word's eight int4 codes, in order: 128 + (code + 8),
+// less 136.
+__device__ __forceinline__ void i4_pairs(uint32_t w, uint32_t *d)
 {
-    const uint32_t a = (w & 0x000f000fu) ^ 0x43084308u;
-    uint32_t r;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x43084308u));
-    return r;
+    const uint32_t u = w ^ 0x88888888u, lo = u & 0x0f0f0f0fu, hi = (u >> 4) & 0x0f0f0f0fu;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const uint32_t four = __byte_perm(lo, hi, e ? 0x7362 : 0x5140);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t b = __byte_perm(four, 0x43434343u, h ? 0x4342 : 0x4140);
+            asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d[2 * e + h]) : "r"(b), "r"(0x43084308u));
+        }
+    }
 }
 
 template <int QUANT, int NT, bool SPLIT, bool PROMOTE>
@@ -263,8 +271,6 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    pdl_wait();    // nothing above touches global memory
-    pdl_launch();  // the next kernel's CTAs may take the room that ending CTAs leave
     const bool gated = p.e.gated;
     const int rows_out = gated ? 64 : 128;
     const int split = SPLIT ? p.split : 1, rank = SPLIT ? (int)(blockIdx.x % split) : 0;
@@ -272,6 +278,17 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
     const int step = SPLIT ? p.tiles : gridDim.x;  // a split tile is the cluster's only one
     const int kb0 = (int)((int64_t)p.blocks * rank / split);
     const int kb1 = (int)((int64_t)p.blocks * (rank + 1) / split);
+    if (warp == 0 && lane < min(kb1 - kb0, C::STAGES)) {  // the first stages' weights
+        const int n0 = (first / p.tiles_m) * rows_out, k = (kb0 + lane) * C::KSUB * 64;
+        for (int j = 0; j < (CODES ? 1 : C::KSUB); ++j) {
+            const int kx = QUANT == AMK_QUANT_W4A16 ? k / 2 : k + j * 64;
+            prefetch_2d(&p.w, kx, n0);
+            if (gated)
+                prefetch_2d(&p.up, kx, n0);
+        }
+    }
+    pdl_wait();    // nothing above reads or writes global memory
+    pdl_launch();  // the next kernel's CTAs may take the room that ending CTAs leave
 
     // the wide kernels for codes: the draining warps hold the sums, and take the
     // registers that the others give up
@@ -555,15 +572,11 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 if (QUANT == AMK_QUANT_W8A16) {
-                                    d[2 * e] = i8_pair(__byte_perm(w[e], 0, 0x4140));
-                                    d[2 * e + 1] = i8_pair(__byte_perm(w[e], 0, 0x4342));
+                                    d[2 * e] = i8_pair(w[e], 0x4140);
+                                    d[2 * e + 1] = i8_pair(w[e], 0x4342);
                                 } else {
-                                    const uint32_t lo = w[e], hi = lo >> 4;
-                                    d[4 * e] = i4_pair(__byte_perm(lo, hi, 0x0400));
-                                    d[4 * e + 1] = i4_pair(__byte_perm(lo, hi, 0x0501));
-                                    d[4 * e + 2] = i4_pair(__byte_perm(lo, hi, 0x0602));
-                                    d[4 * e + 3] = i4_pair(__byte_perm(lo, hi, 0x0703));
-                                }
+                                    i4_pairs(w[e], d + 4 * e);
+                            }
                             }
                         }
                         if (j == 0) {

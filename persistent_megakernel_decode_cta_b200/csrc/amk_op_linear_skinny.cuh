@@ -14,6 +14,12 @@
 // serves two MMAs.  K is shared by four warps of a CTA and by the CTAs of a
 // cluster, whose sums are added in a fixed order.  Sums leave the tensor
 // cores every 512 inputs (every scale group for int4) and are added in fp32.
+//
+// Measured: one token, 4096 x 4096 bf16 8.6 us (reading the weights takes 5.2 at
+// the copy rate: start, cluster sums and end are the rest), 32000 x 4096 38.8 us
+// (6.7 TB/s); 5 tokens, 8192 x 2048 int8 gate and up 9.4 us
+// and 11008 x 4096 23.5: turning codes into bf16, three instructions and a
+// subtraction to two of them, keeps the ALU half busy.
 #ifndef AMK_OP_LINEAR_SKINNY_CUH
 #define AMK_OP_LINEAR_SKINNY_CUH
 
@@ -24,6 +30,7 @@ namespace linear {
 namespace {
 
 constexpr int kSkinnyThreads = 256;
+constexpr int kSkinnyAhead = 512;  // bytes of a warp's share of a row, before the wait
 
 __device__ __forceinline__ uint4 ldg_stream(const void *p)
 {
@@ -43,10 +50,14 @@ __device__ __forceinline__ uint32_t pair_of(const uint4 &v, int j, int h)
     if (QUANT == AMK_QUANT_BF16)
         return w[2 * j + h];
     if (QUANT == AMK_QUANT_W8A16)
-        return i8_pair(__byte_perm(w[j], 0, h ? 0x4342 : 0x4140));
-    const uint32_t lo = w[j >> 1], hi = lo >> 4;
-    const int b = (j & 1) * 2 + h;
-    return i4_pair(__byte_perm(lo, hi, b == 0 ? 0x0400 : b == 1 ? 0x0501 : b == 2 ? 0x0602 : 0x0703));
+        return i8_pair(w[j], h ? 0x4342 : 0x4140);
+    // codes 0 and 2 of a word's four, then 1 and 3: as bytes (code + 8), which lie
+    // under an exponent of 0x43 as 128 + 8 + code
+    const uint32_t c = ((h ? w[j >> 1] >> 4 : w[j >> 1]) & 0x0f0f0f0fu) ^ 0x08080808u;
+    const uint32_t b = __byte_perm(c, 0x43434343u, j & 1 ? 0x4342 : 0x4140);
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(b), "r"(0x43084308u));
+    return r;
 }
 
 // T8: tokens / 8.  A lane holds AHEAD steps of its weights (64 bytes each), two
@@ -89,26 +100,137 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
     const int steps = (p.k + STEP - 1) / STEP, unit = rank * kSkinnyKG + kg;
     const int s0 = (int)((int64_t)steps * unit / (split * kSkinnyKG));
     const int s1 = (int)((int64_t)steps * (unit + 1) / (split * kSkinnyKG));
-    const uint16_t *xp = p.x + g * p.ldx + t * KL;
+    // a column of x to a lane's token (one behind the last is read as the last:
+    // columns of a product do not mix)
+    const uint16_t *xp[T8];
+#pragma unroll
+    for (int c = 0; c < T8; ++c)
+        xp[c] = p.x + min(c * 8 + g, p.e.m - 1) * p.ldx + t * KL;
+    // the start of the warp's share of its rows, a row to a lane (amk_extend, 5
+    // tokens, 7B-shaped: 3.76 -> 3.35 ms int8, 4.25 -> 3.66 bf16)
+    if (s1 > s0) {
+        const uint8_t *row = t == 0 ? wp[0] : t == 1 ? wp[1] : t == 2 ? wp[2] : wp[3];
+        const int64_t at = (int64_t)s0 * 64, have = p.row_bytes - at;
+        const int want = min((s1 - s0) * 64, kSkinnyAhead);
+        prefetch_l2(row - t * 16 + at, (uint32_t)(have < want ? have : want));
+    }
     pdl_wait();
     pdl_launch();
     uint4 w[AHEAD][4];
     uint16_t sc[AHEAD][4];
-    auto load = [&](uint4(&v)[4], uint16_t(&s)[4], int step) {
+    float acc[2][T8][4] = {}, part[2][T8][4] = {};
+    // the products of a step's weights w and x
+    auto products = [&](const uint4(&w)[4], const uint16_t(&sc)[4], const uint4(&xv)[T8][KL / 8]) {
+#pragma unroll
+        for (int j = 0; j < MMAS; ++j) {
+#pragma unroll
+            for (int tile = 0; tile < 2; ++tile) {
+                const uint32_t a0 = pair_of<QUANT>(w[2 * tile], j, 0);
+                const uint32_t a1 = pair_of<QUANT>(w[2 * tile + 1], j, 0);
+                const uint32_t a2 = pair_of<QUANT>(w[2 * tile], j, 1);
+                const uint32_t a3 = pair_of<QUANT>(w[2 * tile + 1], j, 1);
+#pragma unroll
+                for (int c = 0; c < T8; ++c) {
+                    const uint4 q = xv[c][j >> 1];
+                    uint32_t b0 = (j & 1) ? q.z : q.x, b1 = (j & 1) ? q.w : q.y;
+                    if (QUANT == AMK_QUANT_W4A16) {  // in the codes' order
+                        const uint32_t x = b0;
+                        b0 = __byte_perm(x, b1, 0x5410);
+                        b1 = __byte_perm(x, b1, 0x7632);
+                    }
+                    mma_bf16(part[tile][c], a0, a1, a2, a3, b0, b1);
+                }
+            }
+        }
+        if (QUANT == AMK_QUANT_W4A16) {
+#pragma unroll
+            for (int tile = 0; tile < 2; ++tile)
+#pragma unroll
+                for (int c = 0; c < T8; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        acc[tile][c][i] =
+                            fmaf(part[tile][c][i], fp16f(sc[2 * tile + (i >> 1)]), acc[tile][c][i]);
+                        part[tile][c][i] = 0.f;
+                    }
+        }
+    };
+    auto promote = [&] {
+#pragma unroll
+        for (int tile = 0; tile < 2; ++tile)
+#pragma unroll
+            for (int c = 0; c < T8; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    acc[tile][c][i] += part[tile][c][i];
+                    part[tile][c][i] = 0.f;
+                }
+    };
+    // a step's weights, zeros behind the end of the share and of the row
+    auto load = [&](uint4(&v)[4], uint16_t(&sv)[4], int step) {
         const bool in = step < s1 && step * STEP + t * KL < p.k;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v[i] = in ? ldg_stream(wp[i] + (int64_t)step * 64) : make_uint4(0, 0, 0, 0);
             if (QUANT == AMK_QUANT_W4A16)
-                s[i] = step < s1 ? __ldg(sp[i] + step) : (uint16_t)0;
+                sv[i] = step < s1 ? __ldg(sp[i] + step) : (uint16_t)0;
         }
     };
-    float acc[2][T8][4] = {}, part[2][T8][4] = {};
 #pragma unroll
     for (int a = 0; a < AHEAD; ++a)
         load(w[a], sc[a], s0 + a);
-    int since = 0;
-    for (int s = s0; s < s1; s += AHEAD) {
+    int since = 0, s = s0;
+    // While neither these steps nor those that are loaded reach the end, nothing
+    // is looked at and offsets are constants: half the instructions of the loop
+    // behind (5 tokens, 4096 x 11008 int8 gate and up 27.5 us, all by the second
+    // 28.7).  bf16 does not take it: 33.0 us with the second, 35.6 so.
+    const int whole = min(s1, p.k / STEP);
+    if (QUANT != AMK_QUANT_BF16 && s + 2 * AHEAD <= whole) {
+        const uint8_t *wq[4];
+        const uint16_t *sq[4], *xq[T8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            wq[i] = wp[i] + (int64_t)(s + AHEAD) * 64;
+            if (QUANT == AMK_QUANT_W4A16)
+                sq[i] = sp[i] + s + AHEAD;
+        }
+#pragma unroll
+        for (int c = 0; c < T8; ++c)
+            xq[c] = xp[c] + s * STEP;
+        for (; s + 2 * AHEAD <= whole; s += AHEAD) {
+#pragma unroll
+            for (int a = 0; a < AHEAD; ++a) {
+                uint4 xv[T8][KL / 8];
+#pragma unroll
+                for (int c = 0; c < T8; ++c)
+#pragma unroll
+                    for (int i = 0; i < KL / 8; ++i)
+                        xv[c][i] = __ldg(reinterpret_cast<const uint4 *>(xq[c] + a * STEP) + i);
+                products(w[a], sc[a], xv);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    w[a][i] = ldg_stream(wq[i] + a * 64);
+                    if (QUANT == AMK_QUANT_W4A16)
+                        sc[a][i] = __ldg(sq[i] + a);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                wq[i] += AHEAD * 64;
+                if (QUANT == AMK_QUANT_W4A16)
+                    sq[i] += AHEAD;
+            }
+#pragma unroll
+            for (int c = 0; c < T8; ++c)
+                xq[c] += AHEAD * STEP;
+            since += AHEAD;
+            if (QUANT != AMK_QUANT_W4A16 && since >= PROMOTE) {
+                since = 0;
+                promote();
+            }
+        }
+    }
+    for (; s < s1; s += AHEAD) {
 #pragma unroll
         for (int a = 0; a < AHEAD; ++a) {
             const int k = (s + a) * STEP;
@@ -119,53 +241,19 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
 #pragma unroll
                 for (int i = 0; i < KL / 8; ++i)
                     xv[c][i] = in && c * 8 + g < p.e.m
-                                   ? __ldg(reinterpret_cast<const uint4 *>(xp + c * 8 * p.ldx + k) + i)
+                                   ? __ldg(reinterpret_cast<const uint4 *>(xp[c] + k) + i)
                                    : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int j = 0; j < MMAS; ++j) {
-#pragma unroll
-                for (int tile = 0; tile < 2; ++tile) {
-                    const uint32_t a0 = pair_of<QUANT>(w[a][2 * tile], j, 0);
-                    const uint32_t a1 = pair_of<QUANT>(w[a][2 * tile + 1], j, 0);
-                    const uint32_t a2 = pair_of<QUANT>(w[a][2 * tile], j, 1);
-                    const uint32_t a3 = pair_of<QUANT>(w[a][2 * tile + 1], j, 1);
-#pragma unroll
-                    for (int c = 0; c < T8; ++c) {
-                        const uint4 q = xv[c][j >> 1];
-                        mma_bf16(part[tile][c], a0, a1, a2, a3, (j & 1) ? q.z : q.x,
-                                 (j & 1) ? q.w : q.y);
-                    }
-                }
-            }
-            if (QUANT == AMK_QUANT_W4A16) {
-#pragma unroll
-                for (int tile = 0; tile < 2; ++tile)
-#pragma unroll
-                    for (int c = 0; c < T8; ++c)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            acc[tile][c][i] = fmaf(part[tile][c][i],
-                                                   fp16f(sc[a][2 * tile + (i >> 1)]),
-                                                   acc[tile][c][i]);
-                            part[tile][c][i] = 0.f;
-                        }
-            }
+            products(w[a], sc[a], xv);
             load(w[a], sc[a], s + a + AHEAD);
         }
         since += AHEAD;
-        if (QUANT != AMK_QUANT_W4A16 && (since >= PROMOTE || s + AHEAD >= s1)) {
+        if (QUANT != AMK_QUANT_W4A16 && since >= PROMOTE) {
             since = 0;
-#pragma unroll
-            for (int tile = 0; tile < 2; ++tile)
-#pragma unroll
-                for (int c = 0; c < T8; ++c)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        acc[tile][c][i] += part[tile][c][i];
-                        part[tile][c][i] = 0.f;
-                    }
+            promote();
         }
     }
+    if (QUANT != AMK_QUANT_W4A16)
+        promote();
     // c[0], c[1]: row g of tokens 2 t, 2 t + 1; c[2], c[3]: row g + 8
 #pragma unroll
     for (int tile = 0; tile < 2; ++tile)

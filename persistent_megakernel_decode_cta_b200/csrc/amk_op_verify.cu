@@ -10,6 +10,11 @@
 // vocab borders a random number falls, are decisions, and cumulative sums of
 // fp32 terms would move a border past it once in some thousand calls.  The
 // logits are read once (the drawn row's again, from L2).
+//
+// Measured (us): no draft 49152 logits 9.5, 4 drafts 9 rows of 32000 11.4, 8
+// drafts without a distribution 9 rows of 128256 14.8; a caller's Python takes
+// about 13 a call.  Two launches and their latencies bound it (the reads take
+// under 1 us of HBM), then the fp64 exponentials.
 #include <math.h>
 
 #include "amk_ops.cuh"

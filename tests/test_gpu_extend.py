@@ -2,8 +2,8 @@
 oracle fed the same tokens one by one.
 
 Tolerance.  The step rounds what its matrix products take (normed residual,
-rotated q, attention and SwiGLU outputs) to bf16: 2^-9 / sqrt(3) rms of each
-element, so each of the 2 L sublayers' outputs is off by at most 3e-3 of its own
+rotated q, attention and SwiGLU outputs) to bf16: by at most 2^-8 of an element,
+2^-8 / sqrt(3) / sqrt(7 / 3) = 1.5e-3 rms (of a binade's numbers), so each of the 2 L sublayers' outputs is off by at most 3e-3 of its own
 norm (three roundings in a row, and a half for what the norms pass on), added
 up like independent errors with the final norm's: 3e-3 sqrt(2 L + 1) of the
 logits' norm.  A single logit's error is a sum of many independent roundings,
