@@ -869,7 +869,11 @@ extern "C" int amk_extend(amk_handle *h, const int32_t *tokens, int32_t n, int32
         const int32_t m = std::min(h->ext.chunk, n - i);
         // of this chunk's tokens, those among the last n_logits of the call
         const int32_t first = std::max(i, n - n_logits), want = std::max(0, i + m - first);
-        e = cudaMemcpyAsync(h->ext.tokens, tokens + i, sizeof(int32_t) * (size_t)m,
+        // from pageable memory, which the copy reads before it returns: the
+        // caller's may be pinned, and would be read when its turn comes
+        int32_t staged[kExtendChunk];
+        std::memcpy(staged, tokens + i, sizeof(int32_t) * (size_t)m);
+        e = cudaMemcpyAsync(h->ext.tokens, staged, sizeof(int32_t) * (size_t)m,
                             cudaMemcpyHostToDevice, h->stream);
         if (e != cudaSuccess)
             return cuda_fail(e, "amk_extend");

@@ -10,6 +10,7 @@ logits' norm.  A single logit's error is a sum of many independent roundings,
 so nearly normal: none of the some 1e6 that are looked at here is beyond six
 times the root mean square (2e-9 each).
 """
+import ctypes
 import math
 
 import numpy as np
@@ -350,3 +351,18 @@ def test_window_refusals():
         amk.Plan(TINY, 148, amk.default_options(attn_window=-1))
     with pytest.raises(amk.AmkError):
         amk.Plan(TINY, 148, amk.default_options(attn_window=4, attn_sinks=-1))
+
+
+def test_tokens_are_read_before_the_call_returns():
+    dec, _, _ = pair(TINY)
+    toks = si.make_prompt(TINY, 24)
+    want = dec.extend(toks, 0, n_logits=24).clone()
+    pinned = torch.tensor(toks, dtype=torch.int32).pin_memory()
+    got = torch.empty((24, TINY.vocab), device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)  # some 10 ms of work before it on the stream
+    at = ctypes.cast(pinned.data_ptr(), ctypes.POINTER(ctypes.c_int32))
+    assert amk.abi.lib().amk_extend(dec._h, at, 24, 0, 24, got.data_ptr()) == 0
+    pinned.fill_(0)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
