@@ -279,6 +279,7 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
     const int kb0 = (int)((int64_t)p.blocks * rank / split);
     const int kb1 = (int)((int64_t)p.blocks * (rank + 1) / split);
     if (warp == 0 && lane < min(kb1 - kb0, C::STAGES)) {  // the first stages' weights
+        // (17 tokens, 11008 x 4096 int4 gate and up 41.0 us without, 40.1 with)
         const int n0 = (first / p.tiles_m) * rows_out, k = (kb0 + lane) * C::KSUB * 64;
         for (int j = 0; j < (CODES ? 1 : C::KSUB); ++j) {
             const int kx = QUANT == AMK_QUANT_W4A16 ? k / 2 : k + j * 64;

@@ -30,7 +30,6 @@ namespace linear {
 namespace {
 
 constexpr int kSkinnyThreads = 256;
-constexpr int kSkinnyAhead = 512;  // bytes of a warp's share of a row, before the wait
 
 __device__ __forceinline__ uint4 ldg_stream(const void *p)
 {
@@ -106,14 +105,6 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
 #pragma unroll
     for (int c = 0; c < T8; ++c)
         xp[c] = p.x + min(c * 8 + g, p.e.m - 1) * p.ldx + t * KL;
-    // the start of the warp's share of its rows, a row to a lane (amk_extend, 5
-    // tokens, 7B-shaped: 3.76 -> 3.35 ms int8, 4.25 -> 3.66 bf16)
-    if (s1 > s0) {
-        const uint8_t *row = t == 0 ? wp[0] : t == 1 ? wp[1] : t == 2 ? wp[2] : wp[3];
-        const int64_t at = (int64_t)s0 * 64, have = p.row_bytes - at;
-        const int want = min((s1 - s0) * 64, kSkinnyAhead);
-        prefetch_l2(row - t * 16 + at, (uint32_t)(have < want ? have : want));
-    }
     pdl_wait();
     pdl_launch();
     uint4 w[AHEAD][4];

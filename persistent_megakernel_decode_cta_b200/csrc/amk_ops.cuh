@@ -273,11 +273,7 @@ __device__ __forceinline__ void pdl_launch()
 }
 
 // What a kernel that waits will read soon may come into L2 meanwhile, whoever
-// still writes it: L2 is where its reads will look.  size: a multiple of 16.
-__device__ __forceinline__ void prefetch_l2(const void *p, uint32_t size)
-{
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(size) : "memory");
-}
+// still writes it: L2 is where its reads will look.
 __device__ __forceinline__ void prefetch_2d(const void *m, int x, int y)
 {
     asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(m), "r"(x),
