@@ -172,9 +172,9 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
         load(w[a], sc[a], s0 + a);
     int since = 0, s = s0;
     // While neither these steps nor those that are loaded reach the end, nothing
-    // is looked at and offsets are constants: half the instructions of the loop
-    // behind (5 tokens, 4096 x 11008 int8 gate and up 27.5 us, all by the second
-    // 28.7).  bf16 does not take it: 33.0 us with the second, 35.6 so.
+    // is looked at and offsets are constants (5 tokens, 4096 x 11008 int8 gate and
+    // up 27.5 us, all by the loop behind 28.7; 13 tokens, 4096 x 4096 int8 9.2 and
+    // 10.6).  bf16 does not take it: its registers spill, 35.6 us instead of 33.0.
     const int whole = min(s1, p.k / STEP);
     if (QUANT != AMK_QUANT_BF16 && s + 2 * AHEAD <= whole) {
         const uint8_t *wq[4];

@@ -156,6 +156,22 @@ def test_linear_non_finite_inputs_stay_in_their_rows():
     assert not torch.isfinite(y[7].float()).any() and torch.isnan(y[9].float()).all()
 
 
+@pytest.mark.parametrize("fmt,k", [("bf16", 4104), ("int8", 4112), ("int8", 5616), ("int4", 4128),
+                                   ("int4", 10976)])
+def test_linear_few_tokens_over_long_ragged_rows(fmt, k):
+    # rows that end inside a step, behind many whole ones
+    for m in (1, 5, 8, 9, 16):
+        check_linear(m, 200, k, fmt, seed=m + k, gated=m % 2 == 1, out_dtype=F32)
+    x = randn(gen(k), 11, k, dtype=BF16)
+    w, s = weights(fmt, 200, k, k)
+    clean = amk.linear(x, w, scale=s)
+    x[10, k - 1] = math.nan  # the last token, whose row stands in for those behind it
+    x[3, 0] = math.inf
+    y = amk.linear(x, w, scale=s)
+    rows = [i for i in range(11) if i not in (3, 10)]
+    assert torch.equal(y[rows], clean[rows]) and torch.isnan(y[10].float()).all()
+
+
 def test_linear_repeats_bit_for_bit():
     g = gen(6)
     for m in (1, 12, 300):
