@@ -191,6 +191,13 @@ struct Cfg {
     static constexpr int ROOM = (CTAS == 2 ? 112 * 1024 : 224 * 1024) - 2048 - XCH;
     static constexpr int FIT = ROOM / STAGE;
     static constexpr int STAGES = FIT > 8 ? 8 : FIT;
+    // Barriers of landed stages.  Two groups of converting warps take the stages
+    // by turns, and each waits for its own alone, by the parity of the barrier's
+    // phase: the use before must have been its own too, or it could take a still
+    // older phase for this one (copies land in any order).  An odd ring's uses of
+    // a stage alternate between the groups and take two barriers in turn.
+    static constexpr int FULLS = RAW && STAGES % 2 ? 2 * STAGES : STAGES;
+    static_assert(!RAW || FULLS % 2 == 0, "a barrier of landed stages belongs to one group");
     static constexpr int SMEM = STAGES * STAGE + XCH + 1024;
     static constexpr int EW = NT >= 64 ? 2 : 1;  // draining warpgroups
     static constexpr int NC = NT / EW;           // columns of each
@@ -231,7 +238,7 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
     using C = Cfg<QUANT, NT, SPLIT, PROMOTE>;
     constexpr bool CODES = QUANT != AMK_QUANT_BF16;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * C::STAGES + 2 * C::ASTAGES + 2 * C::NB];
+    __shared__ __align__(8) uint64_t bars[C::FULLS + C::STAGES + 2 * C::ASTAGES + 2 * C::NB];
     __shared__ uint32_t tmem_slot;
     __shared__ int fail_flag;
     volatile int *fail = &fail_flag;
@@ -239,18 +246,19 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
     const uint32_t xch = ring + C::STAGES * C::STAGE;
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8 * s; };
-    auto empty = [&](int s) { return bar0 + 8 * (C::STAGES + s); };
-    auto afull = [&](int s) { return bar0 + 8 * (2 * C::STAGES + s); };
-    auto aempty = [&](int s) { return bar0 + 8 * (2 * C::STAGES + C::ASTAGES + s); };
-    auto accf = [&](int b) { return bar0 + 8 * (2 * C::STAGES + 2 * C::ASTAGES + b); };
-    auto acce = [&](int b) { return bar0 + 8 * (2 * C::STAGES + 2 * C::ASTAGES + C::NB + b); };
+    constexpr int RING = C::FULLS + C::STAGES;
+    auto empty = [&](int s) { return bar0 + 8 * (C::FULLS + s); };
+    auto afull = [&](int s) { return bar0 + 8 * (RING + s); };
+    auto aempty = [&](int s) { return bar0 + 8 * (RING + C::ASTAGES + s); };
+    auto accf = [&](int b) { return bar0 + 8 * (RING + 2 * C::ASTAGES + b); };
+    auto acce = [&](int b) { return bar0 + 8 * (RING + 2 * C::ASTAGES + C::NB + b); };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         fail_flag = 0;
-        for (int s = 0; s < C::STAGES; ++s) {
+        for (int s = 0; s < C::FULLS; ++s)
             mbar_init(full(s), 1);
+        for (int s = 0; s < C::STAGES; ++s)
             mbar_init(empty(s), 1 + C::CW / 2);  // the MMAs, and the stage's converting warps
-        }
         for (int s = 0; s < C::ASTAGES; ++s) {
             mbar_init(afull(s), C::CW / 2);
             mbar_init(aempty(s), 1);
@@ -298,7 +306,7 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
             setmaxnreg_to<C::REGS, 40>();
         if (warp == 0) {
             uint32_t it = 0, ph = 1;
-            int s = 0;
+            int s = 0, turn = 0;  // turn: STAGES on an odd ring's second barriers
             bool ok = true;
             for (int tile = first; tile < p.tiles && ok; tile += step) {
                 const int n0 = (tile / p.tiles_m) * rows_out, m0 = (tile % p.tiles_m) * NT;
@@ -308,37 +316,40 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
                         break;
                     }
                     const uint32_t xs = ring + s * C::STAGE, ws = xs + C::X;
+                    const uint32_t landed = full(s + turn);
                     const int k = kb * C::KSUB * 64;
                     if (elect_one()) {
-                        mbar_expect_tx(full(s), C::STAGE);
+                        mbar_expect_tx(landed, C::STAGE);
                         if (CODES) {
                             const int kx = QUANT == AMK_QUANT_W8A16 ? k : k / 2;
-                            tma_2d(ws, &p.w, kx, n0, full(s));
+                            tma_2d(ws, &p.w, kx, n0, landed);
                             if (gated)
-                                tma_2d(ws + C::RAW / 2, &p.up, kx, n0, full(s));
+                                tma_2d(ws + C::RAW / 2, &p.up, kx, n0, landed);
                         }
 #pragma unroll
                         for (int j = 0; j < C::KSUB; ++j) {
                             if (!CODES) {
-                                tma_2d(ws + j * C::BLK, &p.w, k + j * 64, n0, full(s));
+                                tma_2d(ws + j * C::BLK, &p.w, k + j * 64, n0, landed);
                                 if (gated)
                                     tma_2d(ws + j * C::BLK + C::BLK / 2, &p.up, k + j * 64, n0,
-                                           full(s));
+                                           landed);
                             }
-                            tma_2d(xs + j * NT * 128, &p.x, k + j * 64, m0, full(s));
+                            tma_2d(xs + j * NT * 128, &p.x, k + j * 64, m0, landed);
                         }
                     }
                     __syncwarp();
                     if (++s == C::STAGES) {
                         s = 0;
                         ph ^= 1;
+                        if (C::FULLS != C::STAGES)
+                            turn ^= C::STAGES;
                     }
                 }
             }
             if (!ok && lane == 0)  // no copy may land after the CTA has gone
                 for (uint32_t j = it > C::STAGES ? it - C::STAGES : 0; j < it; ++j) {
                     const long long t0 = clock64();
-                    while (!mbar_try_wait(full(j % C::STAGES), (j / C::STAGES) & 1) &&
+                    while (!mbar_try_wait(full(j % C::FULLS), (j / C::FULLS) & 1) &&
                            clock64() - t0 < 2000000000ll) {
                     }
                 }
@@ -546,12 +557,12 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
         const uint32_t dst =
             tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::NB * NT + grp * C::ACOLS;
         uint32_t it = 0, ph = 0, aph = 1;
-        int s = 0;
+        int s = 0, turn = 0;  // as the copies' warp counts them
         bool ok = true;
         for (int tile = first; tile < p.tiles && ok; tile += step)
             for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
                 if ((it & 1) == grp) {
-                    if (!warp_wait(full(s), ph, fail)) {
+                    if (!warp_wait(full(s + turn), ph, fail)) {
                         ok = false;
                         break;
                     }
@@ -599,7 +610,10 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
                 }
                 if (++s == C::STAGES) {
                     s = 0;
-                    ph ^= 1;
+                    if (C::FULLS != C::STAGES)
+                        turn ^= C::STAGES;
+                    if (turn == 0)
+                        ph ^= 1;
                 }
             }
     }

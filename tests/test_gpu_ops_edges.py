@@ -1,0 +1,31 @@
+"""The operators of the multi-token step on the GPU, at the edges of their variants, limits and
+entry points (64-bit forms and tolerances: tests/ops_oracle.py)."""
+import pytest
+import torch
+
+import persistent_megakernel_decode_cta_b200 as amk
+from tests import ops_oracle as oo
+from tests.test_gpu_ops import BF16, close, gen, randn, weights
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _cuda(cuda_ok):
+    torch.backends.cuda.matmul.allow_tf32 = False
+
+
+# int8 weights with bf16 results and many tiles: 192 tokens to a tile, a ring of three stages
+@pytest.mark.parametrize("m,n,k,gated", [(192, 18944, 1024, False), (576, 6272, 2048, False),
+                                         (1000, 1408, 2048, True), (1111, 4000, 656, True)])
+def test_linear_three_stage_ring(m, n, k, gated):
+    x = randn(gen(m), m, k, dtype=BF16)
+    w, s = weights("int8", n, k, m)
+    kw = {"scale": s, "act": "silu"}
+    if gated:
+        kw["up"], kw["up_scale"] = weights("int8", n, k, m + 1)
+    first = amk.linear(x, w, **kw)
+    want, tol = oo.linear(x, w, **kw)
+    close(first, want, tol, f"{m}x{n}x{k}")
+    for _ in range(100):
+        assert torch.equal(amk.linear(x, w, **kw), first)
