@@ -490,13 +490,14 @@ AMK_API int amk_ops_timeouts(uint32_t *n);
 /* y = act(x w^T + bias) [* (x up^T + up_bias)] [+ residual]: a matrix product
  * with its epilogue; with `up` the gated pair of projections of an FFN.
  * x is bf16 [m][k], w and up are in one of the model's weight formats with
- * their scales (see amk_weights; rows contiguous, 1 <= n, k; an even k for
- * W4A16), the biases bf16 [n] or NULL.  y and residual (or NULL) are [m][n] in
- * bf16 or fp32, each with its own row stride; residual may be y itself (same
- * pointer, stride and type), otherwise y overlaps no input.  Row strides are
- * in elements and at least the row length.  Sums are fp32 and rounded once,
- * to y's type.  x rows, w rows and their bases at multiples of 16 bytes run
- * on the tensor cores' fast path; any others are taken by a slower kernel. */
+ * their scales (see amk_weights; rows contiguous, 1 <= n, k <= 2^31 - 4096,
+ * above: AMK_ERR_UNSUPPORTED; an even k for W4A16), the biases bf16 [n] or
+ * NULL.  y and residual (or NULL) are [m][n] in bf16 or fp32, each with its own
+ * row stride; residual may be y itself (same pointer, stride and type),
+ * otherwise y overlaps no input.  Row strides are in elements and at least the
+ * row length.  Sums are fp32 and rounded once, to y's type.  x rows, w rows and
+ * their bases at multiples of 16 bytes run on the tensor cores' fast path; any
+ * others are taken by a slower kernel. */
 typedef enum { AMK_DT_BF16 = 0, AMK_DT_F32 = 1 } amk_dtype;
 typedef enum { AMK_ACT_NONE = 0, AMK_ACT_SILU = 1, AMK_ACT_GELU = 2 /* x Phi(x), exact */,
                AMK_ACT_RELU = 3 } amk_act;

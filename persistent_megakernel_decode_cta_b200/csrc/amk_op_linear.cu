@@ -10,6 +10,9 @@ namespace linear {
 namespace {
 
 constexpr int kQ4GroupLog2 = 7;
+// The kernels count n and k in 32 bits, up to a tile or eight stages (of 128
+// inputs) and a share's last steps beyond them: less than 4096 in all.
+constexpr int kMaxSide = INT32_MAX - 4095;
 
 // ---- the kernel for any alignment ---------------------------------------------
 // A 64 x 64 tile of y per CTA, K in blocks of 32, bf16 mma.sync with fp32
@@ -62,7 +65,7 @@ __global__ void __launch_bounds__(128) linear_generic(const GenericParams p)
     const int g = lane >> 2, t = lane & 3;
     const int n0 = blockIdx.x * kGN;
     const int wm = (warp & 1) * 32, wn = (warp >> 1) * 32;
-    for (int m0 = blockIdx.y * kGM; m0 < p.e.m; m0 += gridDim.y * kGM) {
+    for (int64_t m0 = (int64_t)blockIdx.y * kGM; m0 < p.e.m; m0 += (int64_t)gridDim.y * kGM) {
         float acc[MATS][2][4][4] = {};
         float part[QUANT == AMK_QUANT_W4A16 ? MATS : 1][2][4][4] = {};
         for (int k0 = 0; k0 < p.k; k0 += kGK) {
@@ -142,10 +145,10 @@ __global__ void __launch_bounds__(128) linear_generic(const GenericParams p)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                 {
-                    const int m = m0 + wm + i * 16 + g + (r >> 1) * 8;
+                    const int64_t m = m0 + wm + i * 16 + g + (r >> 1) * 8;
                     const int n = n0 + wn + j * 8 + 2 * t + (r & 1);
                     if (m < p.e.m && n < p.e.n)
-                        emit(p.e, row_const(p.e, n), m, n, acc[0][i][j][r],
+                        emit(p.e, row_const(p.e, n), (int)m, n, acc[0][i][j][r],
                              MATS == 2 ? acc[MATS - 1][i][j][r] : 0.f);
                 }
     }
@@ -155,7 +158,7 @@ template <int QUANT>
 cudaError_t launch_generic(const GenericParams &p, cudaStream_t stream)
 {
     const dim3 grid((unsigned)((p.e.n + kGN - 1) / kGN),
-                    (unsigned)min((p.e.m + kGM - 1) / kGM, 65535));
+                    (unsigned)min(((int64_t)p.e.m + kGM - 1) / kGM, (int64_t)65535));
     if (p.e.gated)
         linear_generic<QUANT, 2><<<grid, 128, 0, stream>>>(p);
     else
@@ -172,6 +175,9 @@ int check_linear(const amk_linear_args *a)
         return bad("NULL arguments");
     if (a->m < 0 || a->n < 1 || a->k < 1)
         return bad("m < 0, n < 1 or k < 1");
+    if (a->n > kMaxSide || a->k > kMaxSide)
+        return amk_set_error(AMK_ERR_UNSUPPORTED, "amk_linear: n %d, k %d: at most %d", a->n, a->k,
+                             kMaxSide);
     if (a->quant < AMK_QUANT_BF16 || a->quant > AMK_QUANT_W4A16)
         return bad("unknown weight format");
     if (a->quant == AMK_QUANT_W4A16 && a->k % 2)

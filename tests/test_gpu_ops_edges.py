@@ -29,3 +29,15 @@ def test_linear_three_stage_ring(m, n, k, gated):
     close(first, want, tol, f"{m}x{n}x{k}")
     for _ in range(100):
         assert torch.equal(amk.linear(x, w, **kw), first)
+
+
+def test_linear_as_many_rows_as_there_can_be():
+    """Row indexes up to 2^31 - 2, through the kernel for any alignment (4 GB of x, and of y)."""
+    m = 2**31 - 1
+    x = torch.empty(m, 1, dtype=BF16, device="cuda").random_(0, 100, generator=gen(0))
+    w = torch.tensor([[3.0]], dtype=BF16, device="cuda")
+    y = amk.linear(x, w)
+    torch.cuda.synchronize()
+    step = 1 << 28
+    for i in range(0, m, step):  # whole numbers up to 297: rounded once, as by torch
+        assert torch.equal(y[i:i + step], (x[i:i + step].float() * 3).to(BF16))
