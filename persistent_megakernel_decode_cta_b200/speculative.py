@@ -43,8 +43,12 @@ def generate(target: Decoder, prompt: Sequence[int], n_new: int, *,
     # the operators run on the decoders' stream
     stream = target.stream if target.stream != torch.cuda.current_stream().cuda_stream else None
     vocab, total = target.cfg.vocab, len(seq) + n_new
-    logits = torch.empty((n_draft + 1, vocab), device="cuda")
-    proposed = torch.empty((max(n_draft, 1), vocab), device="cuda")
+    # what the decoders write comes from their stream's pool: work that is pending
+    # on torch's stream, or starts there after an error, never shares its memory
+    with torch.cuda.stream(torch.cuda.ExternalStream(target.stream) if target.stream
+                           else torch.cuda.default_stream()):
+        logits = torch.empty((n_draft + 1, vocab), device="cuda")
+        proposed = torch.empty((max(n_draft, 1), vocab), device="cuda")
     none = torch.empty(0, dtype=torch.int32, device="cuda")
 
     def uniform(n):
