@@ -477,6 +477,15 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
                         mbar_arrive(acce(b));
                 }
             }
+            if constexpr (!SPLIT && !PROMOTE) {
+                ok = warp_wait(accf(sc % C::NB), (sc / C::NB) & 1, fail);
+                tc_fence_after();
+            }
+            // a gated tile's warps meet at barriers below: all of them, or, when a
+            // wait ran out in one, none.  Also, every warp has read both buffers
+            // of the tile before.
+            if (!SPLIT && gated)
+                ok = named_bar_and(1 + wg, 128, ok);
             if (!ok)
                 break;
             if constexpr (SPLIT) {
@@ -487,13 +496,6 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
                     sts32f(ring + (uint32_t)((wg * C::NC + c) * 128 + r) * 4, acc[c]);
             } else {
                 const int b = sc % C::NB;
-                if (!PROMOTE) {
-                    if (!warp_wait(accf(b), (sc / C::NB) & 1, fail)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                }
                 const RowConst rc = row_const(p.e, n);
                 const int cols = min(C::NC, p.e.m - m0 - wg * C::NC);  // tokens there are
                 const bool mine = n < p.e.n && !is_up;
@@ -543,8 +545,6 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(acce(b));
-                if (gated)  // both buffers are read before the next tile writes them
-                    named_bar(1 + wg, 128);
                 ++sc;
             }
         }

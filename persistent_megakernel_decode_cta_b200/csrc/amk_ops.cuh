@@ -332,6 +332,20 @@ __device__ __forceinline__ void named_bar(int id, int threads)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
+// The same, returning whether v is true in all of them.
+__device__ __forceinline__ bool named_bar_and(int id, int threads, bool v)
+{
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %3, 0;\n\t"
+        "bar.red.and.pred q, %1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"(id), "r"(threads), "r"((uint32_t)v)
+        : "memory");
+    return all != 0;
+}
 __device__ __forceinline__ uint4 lds128(uint32_t a)
 {
     uint4 v;
