@@ -482,9 +482,11 @@ AMK_API int amk_decode_step_noalloc(const amk_plan *plan, const amk_weights *w, 
  * a device, AMK_ERR_CUDA if a launch fails. */
 
 /* Every wait of these kernels is for copies and products of their own CTA and
- * is bounded; a CTA that gives one up (after a second: a faulty device) leaves
- * its outputs unwritten and is counted.  *n (host) = such CTAs on the current
- * device since the library was loaded.  Synchronises the device. */
+ * is bounded.  When a CTA gives one up (after a second: a faulty device), it and
+ * the CTAs that share a tile with it write no output that lacks a part, and
+ * are counted.  *n (host) = such CTAs on the current device since the library
+ * was loaded: the calls themselves, amk_extend among them, have returned
+ * before.  Synchronises the device. */
 AMK_API int amk_ops_timeouts(uint32_t *n);
 
 /* y = act(x w^T + bias) [* (x up^T + up_bias)] [+ residual]: a matrix product

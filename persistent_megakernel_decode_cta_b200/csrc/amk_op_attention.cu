@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(TileCfg<HD, WK, GR>::THREADS, (TileCfg<HD, WK,
     if (split == 1) {
         __syncthreads();
     } else {
-        cluster_sync();
+        cluster_sync_failed(fail, split);
         if (tid < nt && !*fail)
             merge_cluster<C::OS>(p, smem_u32(os), smem_u32(mc), r0, nrows, kvh, rank, tid, nt, redo);
         cluster_sync();  // no CTA leaves, or writes below, while another reads
@@ -869,7 +869,7 @@ __global__ void __launch_bounds__(TcCfg<HD>::THREADS, 2)
                     *reinterpret_cast<float4 *>(os + c + e) =
                         make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
-        } else if (ok) {
+        } else if (ok && tn > 0) {
             const float inv = 1.f / l;
             uint16_t *out = a.out + tok * a.o_ts + h * a.o_hs;
             const bool wide = ((uintptr_t)out & 15) == 0;
@@ -918,7 +918,7 @@ __global__ void __launch_bounds__(TcCfg<HD>::THREADS, 2)
     __syncwarp();
     tc_fence_before();
     if (split > 1) {
-        cluster_sync();
+        cluster_sync_failed(fail, split);
         const float *os = reinterpret_cast<const float *>(smem), *ml = os + 128 * C::OS;
         if (!*fail)
             merge_cluster<C::OS>(p, smem_u32(os), smem_u32(ml), r0, nrows, kvh, rank, tid,

@@ -619,11 +619,11 @@ __global__ void __launch_bounds__(Cfg<QUANT, NT, SPLIT, PROMOTE>::THREADS,
     }
     __syncwarp();
     if (SPLIT) {
-        // every rank's sums are in its shared memory
+        // every rank's sums are in its shared memory, unless one gave up a wait
         if (split == 1)
             __syncthreads();
         else
-            cluster_sync();
+            cluster_sync_failed(fail, split);
         const int et = tid - 128;
         if (et >= 0 && et < C::EW * 128 && !*fail) {
             const int tile = first;

@@ -302,6 +302,21 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t smem, uint32_t rank)
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem), "r"(rank));
     return a;
 }
+// cluster_sync of a kernel whose CTAs can give up a wait: behind it *fail, a
+// CTA's flag at the same place in each of the `size`, is set in all of them when
+// it was set in one.  Only a CTA that failed stores anything, each of its threads
+// (more than `size`) to one rank: a loop over the ranks in one thread cost a call
+// that never enters it 1.8 us (one token, 2048 rows: 12.6 instead of 10.7).
+__device__ __forceinline__ void cluster_sync_failed(volatile int *fail, int size)
+{
+    __syncthreads();
+    if (*fail)
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
+                         map_rank(smem_u32(const_cast<const int *>(fail)), threadIdx.x % size)),
+                     "r"(1)
+                     : "memory");
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
 __device__ __forceinline__ float ld_cluster(uint32_t addr)
 {
     float v;

@@ -65,3 +65,14 @@ def test_the_source_agrees_before_its_barriers():
     barriers = [m.start() for m in re.finditer(r"named_bar\(1 \+ wg, 128\)", drain)]
     assert barriers and all(b > agree.end() for b in barriers)
     assert "break" not in drain[agree.end():barriers[-1]]
+
+
+def test_clusters_hear_of_it_before_they_add_up():
+    """In the kernels that wait: the barrier before a cluster's sums are read tells every rank."""
+    csrc = os.path.join(ROOT, "persistent_megakernel_decode_cta_b200", "csrc")
+    for name, merges in (("amk_op_linear.cuh", 1), ("amk_op_attention.cu", 2)):
+        src = open(os.path.join(csrc, name)).read()
+        assert len(re.findall(r"cluster_sync_failed\(fail, split\);", src)) == merges
+        # what is read behind it is read only where no rank failed
+        for part in src.split("cluster_sync_failed(fail, split);")[1:]:
+            assert "!*fail" in part[:part.index("cluster_sync();")]
