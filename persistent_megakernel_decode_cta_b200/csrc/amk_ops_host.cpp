@@ -104,6 +104,10 @@ extern "C" int amk_ops_timeouts(uint32_t *n)
         return amk_set_error(AMK_ERR_INVALID_ARG, "amk_ops_timeouts: NULL");
     if (!sm_count())
         return no_device("amk_ops_timeouts");
+    // the copies below wait for the default stream's work alone
+    const cudaError_t done = cudaDeviceSynchronize();
+    if (done != cudaSuccess)
+        return launch_status(done, "amk_ops_timeouts");
     uint32_t sum = 0;
     for (auto f : {timeouts_attention, linear::timeouts_bf16, linear::timeouts_int8,
                    linear::timeouts_int4}) {

@@ -31,6 +31,17 @@ def test_linear_three_stage_ring(m, n, k, gated):
         assert torch.equal(amk.linear(x, w, **kw), first)
 
 
+def test_the_count_of_timeouts_waits_for_every_stream():
+    amk.ops_timeouts()  # (a first call loads code, which may wait by itself)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)  # some 100 ms
+        done = torch.cuda.Event()
+        done.record()
+    assert amk.ops_timeouts() == 0
+    assert done.query()
+
+
 def test_linear_as_many_rows_as_there_can_be():
     """Row indexes up to 2^31 - 2, through the kernel for any alignment (4 GB of x, and of y)."""
     m = 2**31 - 1
