@@ -15,6 +15,7 @@ from typing import Optional
 from . import AmkError, _check, abi
 
 _I32 = 2**31 - 1
+_F32_TINY, _F32_MAX = 2.0**-149, 2.0**128 - 2.0**104
 _INVALID = abi.ERR["AMK_ERR_INVALID_ARG"]
 _pack_linear = abi.packer(abi.LinearArgs)
 _pack_attention = abi.packer(abi.AttentionArgs)
@@ -222,6 +223,10 @@ def attention(q, k, v, pos: int, *, window: int = 0, sinks: int = 0,
     given).  Leading dimensions may be strided; head_dim is contiguous."""
     if _torch is None:
         _load()
+    if scale is None:
+        scale = 0.0
+    elif not _F32_TINY <= scale <= _F32_MAX:  # the call takes it in 32 bits, where 0 is the default
+        _refuse("attention: scale must be positive and finite in 32 bits")
     dev = _check_tensors("attention", ("q", "k", "v", "out"), (q, k, v, out))
     bf16 = _torch.bfloat16
     if q.dtype is not bf16 or k.dtype is not bf16 or v.dtype is not bf16:
@@ -239,10 +244,6 @@ def attention(q, k, v, pos: int, *, window: int = 0, sinks: int = 0,
                                                               out.stride())
     if hd > 1 and not q1 == k1 == v1 == o1 == 1:
         _refuse("attention: head_dim must be contiguous")
-    if scale is None:
-        scale = 0.0
-    elif not 0 < scale < float("inf"):
-        _refuse("attention: scale must be positive and finite")
     if not 0 <= pos <= rows - T or rows > _I32:
         raise AmkError(abi.ERR["AMK_ERR_POS_RANGE"], f"attention: positions {pos} .. "
                        f"{pos + T - 1} outside the {rows} rows")
@@ -265,12 +266,14 @@ def verify_draft(target_logits, draft_tokens, u, *, draft_logits=None, temperatu
     (amk_verify_draft).  target_logits: fp32 [drafts + 1, vocab];
     draft_tokens: int32 [drafts]; u: fp32 [drafts + 1] in [0, 1);
     draft_logits: fp32 [drafts, vocab], or None when the draft has no
-    distribution.  temperature 0 is greedy.  Returns (tokens int32
+    distribution.  temperature: 0 (greedy), or 1e-6 .. 1e6.  Returns (tokens int32
     [drafts + 1], n_accepted int32 [1]) on the device: the accepted tokens, the
     drawn one, then -1.  With no drafts it samples one token."""
     if _torch is None:
         _load()
     torch = _torch
+    if not (temperature == 0 or 1e-6 <= temperature <= 1e6):  # less could become 0: greedy
+        _refuse("verify_draft: temperature is not 0 or within [1e-6, 1e6]")
     dev = _check_tensors("verify_draft", ("target_logits", "draft_tokens", "u", "draft_logits",
                                           "tokens", "n_accepted"),
                          (target_logits, draft_tokens, u, draft_logits, tokens, n_accepted))
