@@ -334,7 +334,8 @@ AMK_API int amk_decode_step_host(amk_handle *h, int32_t token_id, int32_t pos,
  * (AMK_ERR_UNSUPPORTED).  The first call allocates the activations.  A step
  * that follows with token_id -1 is refused (this call chooses no token: see
  * amk_verify_draft, which does with n_draft 0).  With W4A16 weights the
- * caller's arrays are read. */
+ * caller's arrays are read.  AMK_ERR_UNSUPPORTED, and nothing changed, for
+ * models with head_dim above 256 or max_ctx above 2^30 (amk_attention's). */
 AMK_API int amk_extend(amk_handle *h, const int32_t *tokens, int32_t n, int32_t pos,
                int32_t n_logits, float *logits_dev);
 

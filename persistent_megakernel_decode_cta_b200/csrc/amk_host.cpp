@@ -850,6 +850,10 @@ extern "C" int amk_extend(amk_handle *h, const int32_t *tokens, int32_t n, int32
                                  tokens[i], c.vocab);
     if (n == 0)
         return AMK_OK;
+    if (c.head_dim > amk::kAttentionMaxHd || c.max_ctx > amk::kAttentionMaxRows)
+        return amk_set_error(AMK_ERR_UNSUPPORTED, "amk_extend: heads of %d elements over %d rows, "
+                             "at most %d and %d", c.head_dim, c.max_ctx, amk::kAttentionMaxHd,
+                             amk::kAttentionMaxRows);
     cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
     cudaError_t e = cudaStreamIsCapturing(h->stream, &capturing);
     if (e != cudaSuccess)

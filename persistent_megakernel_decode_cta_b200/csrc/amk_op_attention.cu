@@ -33,8 +33,7 @@ __device__ __forceinline__ void visible(const AttnParams &a, int p, int &s, int 
 // other.  Rows outside the mask are not touched, so nothing they hold can
 // reach the result.  qs: the warp's query in shared memory, pre-scaled, [hd].
 // Writes the elements d for which mine(d).
-constexpr int kMaxHd = 256;
-constexpr int kMaxRows = 1 << 30;  // positions and what is added to them stay in 32 bits
+constexpr int kMaxHd = kAttentionMaxHd, kMaxRows = kAttentionMaxRows;
 
 template <typename Mine>
 __device__ void attend_row(const AttnParams &a, int t, int h, const float *qs, Mine mine)

@@ -44,6 +44,11 @@ bool encode_3d(CUtensorMap *map, CUtensorMapDataType type, const void *base, int
 int sm_count();                    // of the current device; 0: no device
 int no_device(const char *what);   // the status of a call that found no device
 
+// Limits of amk_attention: head sizes, and rows (positions and what is added to
+// them stay in 32 bits).
+constexpr int kAttentionMaxHd = 256;
+constexpr int kAttentionMaxRows = 1 << 30;
+
 // CTAs of the attention and linear kernels that gave up a wait on the current
 // device (each source file counts its own).
 cudaError_t timeouts_attention(uint32_t *n);

@@ -58,3 +58,22 @@ def test_generation_that_fails_leaves_the_decoders_usable():
         amk.generate(target, prompt, 10, temperature=-1.0)
     assert amk.generate(target, prompt, 10, temperature=0.0) == want
     target.close()
+
+
+def test_extend_refuses_wide_heads_before_it_changes_anything():
+    """The single-token step takes heads of 512, the attention over several tokens up to 256."""
+    cfg = TINY.with_(hidden=512, n_heads=2, n_kv_heads=2, head_dim=512, max_ctx=16)
+    dec = amk.Decoder(cfg, si.make_model(cfg, device="cuda"))
+    dec.step(1, 0)
+    before = [t.clone() for layer in range(cfg.n_layers) for t in dec.kv(layer)]
+    with pytest.raises(amk.AmkError, match="UNSUPPORTED"):
+        dec.extend([2, 3, 4], 0)
+    torch.cuda.synchronize()
+    after = [t for layer in range(cfg.n_layers) for t in dec.kv(layer)]
+    assert all(torch.equal(a, b) for a, b in zip(before, after))
+    dec.step(-1, 1)  # the token that the step before chose
+    dec.close()
+    cfg = TINY.with_(hidden=256, n_heads=2, n_kv_heads=1, head_dim=256, max_ctx=16)
+    dec = amk.Decoder(cfg, si.make_model(cfg, device="cuda"))
+    assert torch.isfinite(dec.extend([2, 3, 4], 0, n_logits=3)).all()
+    dec.close()
