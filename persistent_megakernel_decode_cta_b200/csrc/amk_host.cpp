@@ -27,13 +27,13 @@ using amk::KParams;
 using amk::TaskDesc;
 
 extern "C" cudaError_t amk_kernel_configure(int smem_bytes, int quant, int att_e, int generic,
-                                            int fused);
+                                            int fused, int gap);
 extern "C" cudaError_t amk_pack_down(const void *wd, void *out, int h, int ffn, int esz,
                                      cudaStream_t stream);
 extern "C" cudaError_t amk_pack_q4(const void *codes, const void *scales, void *out, int rows,
                                    int K, cudaStream_t stream);
 extern "C" cudaError_t amk_kernel_occupancy(int smem_bytes, int quant, int att_e, int generic,
-                                            int fused, int *blocks_per_sm);
+                                            int fused, int gap, int *blocks_per_sm);
 namespace amk {
 extern "C" cudaError_t amk_kernel_launch(const KParams *p, int n_ctas, int smem_bytes,
                                          cudaStream_t stream);
@@ -429,17 +429,21 @@ extern "C" int amk_create(const amk_config *cfg, const amk_weights *w, const amk
     const amk_plan *P = H->plan;
     const int q8 = P->cfg.quant == AMK_QUANT_W8A16 ? 1 : 0;
     const int qm = P->cfg.quant;  // 0 bf16, 1 int8, 2 int4
-    cudaError_t e = amk_kernel_configure(P->smem_bytes, qm, P->att_e, P->generic, P->ffn_fused);
-    if (e != cudaSuccess) {
-        free_handle(H);
-        return cuda_fail(e, "cudaFuncSetAttribute");
-    }
-    int per_sm = 0;
-    e = amk_kernel_occupancy(P->smem_bytes, qm, P->att_e, P->generic, P->ffn_fused, &per_sm);
-    if (e != cudaSuccess || per_sm < 1) {
-        free_handle(H);
-        return amk_set_error(AMK_ERR_LAUNCH, "kernel does not fit one SM (smem %d B)",
-                             P->smem_bytes);
+    cudaError_t e = cudaSuccess;
+    for (int gap = 0; gap <= (P->opt.attn_window > 0); ++gap) {  // the instances its steps run
+        e = amk_kernel_configure(P->smem_bytes, qm, P->att_e, P->generic, P->ffn_fused, gap);
+        if (e != cudaSuccess) {
+            free_handle(H);
+            return cuda_fail(e, "cudaFuncSetAttribute");
+        }
+        int per_sm = 0;
+        e = amk_kernel_occupancy(P->smem_bytes, qm, P->att_e, P->generic, P->ffn_fused, gap,
+                                 &per_sm);
+        if (e != cudaSuccess || per_sm < 1) {
+            free_handle(H);
+            return amk_set_error(AMK_ERR_LAUNCH, "kernel does not fit one SM (smem %d B)",
+                                 P->smem_bytes);
+        }
     }
     const amk_config &c = P->cfg;
     const int L = c.n_layers, nkv = c.n_kv_heads, hd = c.head_dim;
@@ -702,7 +706,7 @@ int launch_step(amk_handle *H, int32_t token_id, int32_t pos, float *logits_dev,
     k.token = token_id;
     const amk::VisibleRows vis =
         amk::visible_rows(pos, H->plan->opt.attn_window, H->plan->opt.attn_sinks);
-    k.att_n = vis.n;
+    k.att_pos = vis.n - 1;
     k.att_sinks = vis.sinks;
     k.att_gap = vis.gap;
     k.att_chunk = amk::attn_chunk_len(vis.n, H->plan->opt.attn_splits);

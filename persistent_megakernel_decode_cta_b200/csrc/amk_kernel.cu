@@ -16,6 +16,10 @@ const void *amk_kernel_q1_f0(int e);
 const void *amk_kernel_q1_f1(int e);
 const void *amk_kernel_q2_f0(int e);
 const void *amk_kernel_generic();
+const void *amk_kernel_q0_f0_gap(int e);
+const void *amk_kernel_q1_f0_gap(int e);
+const void *amk_kernel_q2_f0_gap(int e);
+const void *amk_kernel_generic_gap();
 
 // Wdown of one layer, [hidden][ffn] row-major, re-laid once per handle as
 // 16-byte column groups, [ffn * esz / 16][hidden][16 B], so that a fused FFN
@@ -39,13 +43,18 @@ extern "C" int amk_kernel_smem_bytes(int ring_stages, int stage_bytes, int vec_f
 }
 
 namespace {
-const void *kernel_for(int quant, int att_e, int generic, int fused)
+// gap: the step's visible cache rows are not one range
+const void *kernel_for(int quant, int att_e, int generic, int fused, int gap)
 {
-    if (generic)
-        return amk_kernel_generic();
+    if (generic || (gap && fused))
+        return gap ? amk_kernel_generic_gap() : amk_kernel_generic();
     int e = 0;
     while (e < 4 && (1 << e) < att_e)
         ++e;
+    if (gap)
+        return quant == 2 ? amk_kernel_q2_f0_gap(e)
+               : quant    ? amk_kernel_q1_f0_gap(e)
+                          : amk_kernel_q0_f0_gap(e);
     if (quant == 2)  // int4 models never take the fused FFN level
         return amk_kernel_q2_f0(e);
     if (quant)
@@ -55,17 +64,17 @@ const void *kernel_for(int quant, int att_e, int generic, int fused)
 }  // namespace
 
 extern "C" cudaError_t amk_kernel_configure(int smem_bytes, int quant, int att_e, int generic,
-                                            int fused)
+                                            int fused, int gap)
 {
-    return cudaFuncSetAttribute(kernel_for(quant, att_e, generic, fused),
+    return cudaFuncSetAttribute(kernel_for(quant, att_e, generic, fused, gap),
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes);
 }
 
 extern "C" cudaError_t amk_kernel_occupancy(int smem_bytes, int quant, int att_e, int generic,
-                                            int fused, int *blocks_per_sm)
+                                            int fused, int gap, int *blocks_per_sm)
 {
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-        blocks_per_sm, kernel_for(quant, att_e, generic, fused), kThreads, smem_bytes);
+        blocks_per_sm, kernel_for(quant, att_e, generic, fused, gap), kThreads, smem_bytes);
 }
 
 extern "C" cudaError_t amk_pack_down(const void *wd, void *out, int h, int ffn, int esz,
@@ -111,9 +120,9 @@ extern "C" cudaError_t amk_kernel_launch(const KParams *p, int n_ctas, int smem_
                                          cudaStream_t stream)
 {
     void *args[] = {const_cast<KParams *>(p)};
-    return cudaLaunchCooperativeKernel(kernel_for(p->quant, p->att_e, p->generic, p->ffn_fused),
-                                       dim3(n_ctas),
-                                       dim3(kThreads), args, (size_t)smem_bytes, stream);
+    return cudaLaunchCooperativeKernel(kernel_for(p->quant, p->att_e, p->generic, p->ffn_fused,
+                                                  p->att_gap != 0),
+                                       dim3(n_ctas), dim3(kThreads), args, (size_t)smem_bytes, stream);
 }
 
 }  // namespace amk

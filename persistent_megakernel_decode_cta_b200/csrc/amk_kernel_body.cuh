@@ -501,14 +501,14 @@ __device__ __forceinline__ Geom task_geom(const KParams &p, const TaskDesc &d)
     Geom g{};
     if (d.kind == TK_ATTN) {
         const int c = d.r1;
-        const int n = p.att_n;          // visible cache rows, this step's last
+        const int n = p.att_pos + 1;    // visible cache rows, this step's last
         const int chunk = p.att_chunk;  // of them per chunk at this step
         g.j0 = c * chunk;
         g.j1 = min(g.j0 + chunk, n);
         if (g.j1 < g.j0)
             g.j1 = g.j0;
         g.pa = g.j0;
-        g.pb = max(g.pa, min(g.j1, n - 1));
+        g.pb = max(g.pa, min(g.j1, p.att_pos));
         g.P = p.att_P;
         g.nchunks = (g.pb - g.pa + g.P - 1) / g.P;
         return g;
@@ -559,6 +559,8 @@ struct Lookahead {
     uint64_t pos;          // stream position of the cursor
 };
 
+// GAP: see producer_loop.
+template <bool GAP>
 __device__ __forceinline__ void lookahead_load(const KParams &p, Lookahead &la)
 {
     const uint8_t *rec = reinterpret_cast<const uint8_t *>(p.tasks + la.ti);
@@ -575,7 +577,8 @@ __device__ __forceinline__ void lookahead_load(const KParams &p, Lookahead &la)
     const uint8_t *w0 = reinterpret_cast<const uint8_t *>(w.x);
     const uint8_t *w1 = reinterpret_cast<const uint8_t *>(w.y);
     if (d.kind == TK_ATTN) {
-        const size_t o = (size_t)(g.pa + (g.pa < p.att_sinks ? 0 : p.att_gap)) * p.head_dim * 2;
+        const int from = GAP && g.pa >= p.att_sinks ? g.pa + p.att_gap : g.pa;
+        const size_t o = (size_t)from * p.head_dim * 2;
         la.a = w0 + o;
         la.b = w1 + o;
         la.na = la.nb = (uint32_t)(g.pb - g.pa) * p.head_dim * 2;
@@ -591,6 +594,7 @@ __device__ __forceinline__ void lookahead_load(const KParams &p, Lookahead &la)
 
 // Advances the cursor to stream position `hi`, prefetching the bytes at or
 // past `lo` (the copy cursor: bytes before it are in the ring already).
+template <bool GAP>
 __device__ __forceinline__ void lookahead_pump(const KParams &p, Lookahead &la, int qe,
                                                uint64_t lo, uint64_t hi)
 {
@@ -599,7 +603,7 @@ __device__ __forceinline__ void lookahead_pump(const KParams &p, Lookahead &la, 
         if (la.part >= 2) {
             if (++la.ti >= qe)
                 return;
-            lookahead_load(p, la);
+            lookahead_load<GAP>(p, la);
             continue;
         }
         const uint8_t *base = la.part ? la.b : la.a;
@@ -681,7 +685,13 @@ __device__ __forceinline__ void flight_push(const SmemLayout &s, Flight &f, uint
 }
 
 // Lane 0 of the producer warpgroup streams every chunk of every task of this
-// SM's queue into the ring, one task record ahead.
+// SM's queue into the ring, one task record ahead.  GAP: the visible cache rows
+// are not one range (a window, further on than its sinks).  A loop of its own,
+// since one thread issues everything and each instruction between two copies
+// counts: one loop for both cost steps without a window 1.1 to 1.4 % (Llama-7B
+// W4A16 at 2048 and at 0: 1897 and 1575 us instead of 1876 and 1550), and both
+// in one kernel bf16 0.6 %, so that each has an instance of the kernel.
+template <bool GAP>
 __device__ void producer_loop(const KParams &p, const SmemLayout &s, int qb, int qe)
 {
     const uint64_t pol_w = evict_first_policy();  // weights: streamed once per step
@@ -727,7 +737,7 @@ __device__ void producer_loop(const KParams &p, const SmemLayout &s, int qb, int
                     if (it == 0) {
                         t0 = gtimer();
                         if (p.lookahead)
-                            lookahead_pump(p, la, qe, cpos, cpos + p.lookahead);
+                            lookahead_pump<GAP>(p, la, qe, cpos, cpos + p.lookahead);
                     }
                     if ((++it & 255) == 0) {
                         if (*abort_flag || gtimer() - t0 > p.timeout_ns * 4 ||
@@ -756,10 +766,7 @@ __device__ void producer_loop(const KParams &p, const SmemLayout &s, int qb, int
                 // K rows on piece 0, V rows on piece 1
                 const int a = g.pa + i * g.P;
                 const int b = min(a + g.P, g.pb);
-                const uint32_t row = (uint32_t)p.head_dim * 2, nb = (uint32_t)(b - a) * row;
-                // visible row v is cache row v among the sinks, v + att_gap behind
-                // them: a range across that border takes two copies
-                const int na = min(max(p.att_sinks - a, 0), b - a);
+                const uint32_t nb = (uint32_t)(b - a) * p.head_dim * 2;
                 for (int h = 0; h < 2 && !stop; ++h) {
                     if (!flight_reserve(p, s, fl, nb, done_below, prof_wait)) {
                         stop = true;
@@ -767,13 +774,22 @@ __device__ void producer_loop(const KParams &p, const SmemLayout &s, int qb, int
                     }
                     const uint32_t bar = bar0 + 8 * h;
                     mbar_arrive_expect_tx(bar, nb);
-                    const uint32_t to = dst + (uint32_t)h * g.P * row;
-                    const uint8_t *from = (h ? w1 : w0) + (size_t)a * row;
-                    if (na > 0)
-                        bulk_g2s_nohint(to, from, na * row, bar);
-                    if (na < b - a)
-                        bulk_g2s_nohint(to + na * row, from + (size_t)(na + p.att_gap) * row,
-                                        nb - na * row, bar);
+                    if constexpr (!GAP) {
+                        bulk_g2s_nohint(dst + (uint32_t)h * g.P * p.head_dim * 2,
+                                        (h ? w1 : w0) + (size_t)a * p.head_dim * 2, nb, bar);
+                    } else {
+                        // visible row v is cache row v among the sinks, v + att_gap behind
+                        // them: a range across that border takes two copies
+                        const int na = min(max(p.att_sinks - a, 0), b - a);
+                        const uint32_t row = (uint32_t)p.head_dim * 2;
+                        const uint32_t to = dst + (uint32_t)h * g.P * row;
+                        const uint8_t *from = (h ? w1 : w0) + (size_t)a * row;
+                        if (na > 0)
+                            bulk_g2s_nohint(to, from, na * row, bar);
+                        if (na < b - a)
+                            bulk_g2s_nohint(to + na * row, from + (size_t)(na + p.att_gap) * row,
+                                            nb - na * row, bar);
+                    }
                     flight_push(s, fl, bar, par, nb, k);
                     ++used;
                 }
@@ -2063,7 +2079,7 @@ __device__ __forceinline__ bool attn_chunk(const KParams &p, const SmemLayout &s
     consumer_bar();
     if (*reinterpret_cast<volatile int *>(s.flags))
         return false;
-    if (g.j0 < p.att_n && p.att_n <= g.j1 && warp == 0) {
+    if (g.j0 <= p.att_pos && p.att_pos < g.j1 && warp == 0) {
         // the new position: K and V rows of this step (bf16 values as
         // floats), taken by position group 0
         float sc = 0.f;
@@ -2121,7 +2137,7 @@ __device__ __forceinline__ bool attn_chunk(const KParams &p, const SmemLayout &s
     consumer_bar();
     // the only non-empty chunk of the step writes the normalised output of
     // its heads directly; otherwise the partial (m, l, o) for the merge
-    const bool direct = g.j0 == 0 && g.j1 == p.att_n;
+    const bool direct = g.j0 == 0 && g.j1 == p.att_pos + 1;
     float *out = p.part + ((((size_t)l * nkv + gi) * p.attn_splits + c) * G) * (hd + 2);
     uint64_t *fin = p.attn + (size_t)l * nh * hd + (size_t)gi * G * hd;
     for (int i = ct; i < G * hd; i += kConsumerThreads) {
@@ -2258,7 +2274,7 @@ __device__ __forceinline__ bool attn_task(const KParams &p, const SmemLayout &s,
     if (!attn_chunk<E>(p, s, d, g, kc, ct, warp, lane, wt, otag))
         return false;
     const int l = d.layer, gi = d.r0, C = p.attn_splits;
-    const int n = p.att_n;
+    const int n = p.att_pos + 1;
     const int chunk = p.att_chunk;
     const int nne = (n + chunk - 1) / chunk;  // non-empty chunks: 0 .. nne-1
     if (nne == 1 || g.j1 <= g.j0)
@@ -2811,8 +2827,9 @@ __device__ __forceinline__ void consumer_loop(const KParams &p, const SmemLayout
 
 // ------------------------------------------------------------------- kernel
 // One fast instance per (weight format, attention lane width), holding only
-// the paths its models use, plus one generic instance for the rest.
-template <int Q8, int ATT_E, int GENERIC, int FUSED>
+// the paths its models use, plus one generic instance for the rest; and the
+// same (GAP) for steps whose visible cache rows are not one range.
+template <int Q8, int ATT_E, int GENERIC, int FUSED, int GAP = 0>
 __global__ void __launch_bounds__(kThreads, 1) amk_decode_kernel(const __grid_constant__ KParams p)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -2838,7 +2855,7 @@ __global__ void __launch_bounds__(kThreads, 1) amk_decode_kernel(const __grid_co
     if (tid < kProducerThreads) {
         setmaxnreg_dec<kProducerRegs>();
         if (tid == 0)
-            producer_loop(p, s, qb, qe);
+            producer_loop<GAP != 0>(p, s, qb, qe);
         return;
     }
     setmaxnreg_inc<kConsumerRegs>();

@@ -23,7 +23,7 @@
 
 extern "C" int amk_kernel_smem_bytes(int ring_stages, int stage_bytes, int vec_floats);
 extern "C" cudaError_t amk_kernel_configure(int smem_bytes, int quant, int att_e, int generic,
-                                            int fused);
+                                            int fused, int gap);
 namespace amk {
 extern "C" cudaError_t amk_kernel_launch(const KParams *p, int n_ctas, int smem_bytes,
                                          cudaStream_t stream);
@@ -361,7 +361,7 @@ extern "C" int amk_decode_step_noalloc(const amk_plan *plan, const amk_weights *
     k.pos = pos;
     k.token = token_id;
     const amk::VisibleRows vis = amk::visible_rows(pos, P.opt.attn_window, P.opt.attn_sinks);
-    k.att_n = vis.n;
+    k.att_pos = vis.n - 1;
     k.att_sinks = vis.sinks;
     k.att_gap = vis.gap;
     k.att_chunk = amk::attn_chunk_len(vis.n, P.opt.attn_splits);
@@ -376,7 +376,8 @@ extern "C" int amk_decode_step_noalloc(const amk_plan *plan, const amk_weights *
     k.lookahead = (uint32_t)(P.opt.l2_prefetch_kb > 0 ? P.opt.l2_prefetch_kb : 0) * 1024u;
     k.inflight = amk_inflight_bytes(&P.opt);
     k.piece = amk_piece_bytes(&P.opt);
-    e = amk_kernel_configure(P.smem_bytes, q8 ? 1 : 0, P.att_e, P.generic, P.ffn_fused);
+    e = amk_kernel_configure(P.smem_bytes, q8 ? 1 : 0, P.att_e, P.generic, P.ffn_fused,
+                             vis.gap != 0);
     if (e != cudaSuccess)
         return fail_cuda(e, "cudaFuncSetAttribute");
     e = amk::amk_kernel_launch(&k, P.n_sms, P.smem_bytes, st);
