@@ -472,7 +472,7 @@ AMK_API int amk_decode_step_noalloc(const amk_plan *plan, const amk_weights *w, 
 /* (No counterpart in the AutoMegaKernel pages, which decode one token per
  * launch: what a caller needs next to that step.)  The matrix product, the
  * attention and the token choice that a step over several tokens is made of,
- * each on caller-owned device memory.  amk_extend (below) runs a handle's
+ * each on caller-owned device memory.  amk_extend (above) runs a handle's
  * model with the first two.  They take no handle, allocate nothing, keep
  * nothing between calls, only enqueue work on cuda_stream (which may be
  * capturing a CUDA graph; the graph then holds the arguments' pointers), and

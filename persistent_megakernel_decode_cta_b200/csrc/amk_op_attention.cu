@@ -117,10 +117,13 @@ __device__ unsigned int g_timeouts;  // CTAs that gave up a wait
 // of stages with TMA (swizzled; rows behind the last token and elements behind
 // head_dim read as 0); GR groups of WK warps take the stages by turns, a warp
 // the tile's 16 rows and a WK-th of the stage's keys: scores, the running
-// maximum and sum of the softmax, and the weighted sum of V, all in registers
-// (weights are rounded to bf16 for the product with V, as tensor cores take
-// them: at most 2^-8 of each; their sum is taken before).  The warps merge through
-// shared memory, the CTAs of a cluster that share the keys of a tile through
+// maximum and sum of the softmax (Milakov and Gimelshein, Online normalizer
+// calculation for softmax, 2018), and the weighted sum of V, all in registers.
+// Weights are rounded to bf16 for the product with V; their sum is taken before.
+// An MMA's operands have one type: weights of more bits would take V as tf32, in
+// twice the shared memory at half the rate.  The rounding is at most 2^-8 of each
+// weight, of either sign, and so no more in their sum than what the output loses
+// when it is rounded to bf16 itself.  The warps merge through shared memory, the CTAs of a cluster that share the keys of a tile through
 // distributed shared memory, in a fixed order.
 //
 // A step of a warp is a chain of dependent instructions (0.4 us for 16 keys),
@@ -579,14 +582,17 @@ cudaError_t launch_tiles(TileParams &p, cudaStream_t stream)
 // shared memory in the layout the MMA reads, and V taken as it lies in the
 // cache (its rows are the K of that product).  A thread of the four softmax
 // warps has a row to itself: maximum and sum need no shuffles.  O is rescaled
-// only when a row's maximum has grown by more than 8 (a factor of 256, exact
-// in fp32 and bf16 alike); until then the weights are taken against the
-// earlier maximum, which the final division by their sum makes good.
+// only when a row's maximum has grown by more than 8 (a published refinement of
+// the running maximum; a factor of 256, exact in fp32 and bf16 alike); until then
+// the weights are taken against the earlier maximum, which the final division by
+// their sum makes good.
 //
-// Measured: 2048 tokens of 32 heads of 128, window 1024 and 4 sinks: 70 us; 2048
-// tokens without a window: 605 TFLOP/s.  The softmax warps bound it: 64 keys of a
-// row are 64 exponentials, maxima and roundings of one thread for 128 x 64 x 128
-// products, and a CTA's products wait for them every 64 keys.
+// Measured: 2048 tokens of 32 heads of 128 from position 0 on, window 1024 and 4
+// sinks 59 us, without a window 58 us (594 TFLOP/s).  No pipe bounds it: tensor
+// cores are busy for 27 % of the cycles, exponentials for 28 %, and a scheduler
+// issues in 32 % of them.  The scores' product, the 64 keys of a thread's softmax
+// and the product with V take turns within a CTA, which the other CTA of the SM
+// covers in part.
 template <int HD>
 struct TcCfg {
     static constexpr int SUB = HD / 64;               // blocks of 64 elements of a head

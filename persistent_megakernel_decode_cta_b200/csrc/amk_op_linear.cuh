@@ -14,11 +14,18 @@
 // the bf16 integers they are (exact) and write them to TMEM, from where the MMA
 // takes its A: shared memory, which bounds these kernels, then carries the codes
 // and x alone (2048 tokens, 4096 x 11008 int8 gate and up: 390 us with A in
-// shared memory, 330 us so; bf16 weights 266 us).  int8 row scales are applied
-// to the sums.  The sums of an int4 row's 128-input groups are scaled apart: each
-// group is a sum of its own (`seg`), which the draining warps scale and add in
-// fp32 registers, and which costs the time between the two (same call: 520 us).
-// So weights are never rounded.
+// shared memory, 313 to 337 us so; bf16 weights 272 us, the tensor cores busy for
+// 81 % of the cycles).  int8 row scales are applied to the sums.  The sums of an
+// int4 row's 128-input groups are scaled apart: each group is a sum of its own
+// (`seg`), which the draining warps scale and add in fp32 registers, and which
+// costs the time between the two (same call: 522 us).  So weights are never
+// rounded.
+//
+// Few tiles of codes are bound by latency: at 77 tokens, 4096 x 11008 int4 (23.7
+// us) and 300 tokens, 4096 x 4096 int8 (22.8) no pipe is busy for more than 41 %
+// of the active cycles, tensor cores and ALU included.  A stage's chain of
+// wait, load, convert, TMEM store, store wait and arrive sets the pace, two of
+// them at a time (a TMEM buffer each).
 //
 // Tensor cores cut off what falls below their accumulators when they align
 // the terms of a sum, always downward in magnitude: over K = 4096 an fp32
@@ -38,6 +45,8 @@ using namespace ops;
 
 __device__ __forceinline__ float activate(int act, float v)
 {
+    // __expf is off by (2 + 1.2 |v|) 2^-23 of its value at most, as in the decode
+    // step's SwiGLU; the rest of a SiLU adds three roundings
     if (act == AMK_ACT_SILU)
         return v / (1.f + __expf(-v));
     if (act == AMK_ACT_GELU)

@@ -15,11 +15,15 @@
 // cluster, whose sums are added in a fixed order.  Sums leave the tensor
 // cores every 512 inputs (every scale group for int4) and are added in fp32.
 //
-// Measured: one token, 4096 x 4096 bf16 8.6 us (reading the weights takes 5.2 at
-// the copy rate: start, cluster sums and end are the rest), 32000 x 4096 38.8 us
-// (6.7 TB/s); 5 tokens, 8192 x 2048 int8 gate and up 9.4 us
-// and 11008 x 4096 23.5: turning codes into bf16, three instructions and a
-// subtraction to two of them, keeps the ALU half busy.
+// Measured: one token, 4096 x 4096 bf16 9.1 us (reading the weights takes 5.2 at
+// the copy rate: start, cluster sums and end are the rest), 32000 x 4096 42.9 us
+// (6.1 TB/s); 5 tokens, 8192 x 2048 int8 gate and up 9.3 us and 11008 x 4096
+// 23.5; one token, 11008 x 4096 int4 gate and up 19.3.  Codes wait for their
+// loads first (int8 4.5 warps to an issue, int4 2.3, two steps being all that the
+// registers hold), then for the instructions that convert them, three and a
+// subtraction to two (the ALU is busy for 50 % of the active cycles); and 344
+// CTAs of 11008 rows on 296 places leave the SMs active for 23 to 36 thousand
+// cycles, 27 on average (int4).
 #ifndef AMK_OP_LINEAR_SKINNY_CUH
 #define AMK_OP_LINEAR_SKINNY_CUH
 
@@ -61,9 +65,11 @@ __device__ __forceinline__ uint32_t pair_of(const uint4 &v, int j, int h)
 
 // T8: tokens / 8.  A lane holds AHEAD steps of its weights (64 bytes each), two
 // CTAs to an SM: 64 KB of weights and more on their way.  Measured (us, AHEAD
-// 2 / 3 / 4): 1 x 32000 x 4096 bf16 45.0 / 42.3 / 41.8, 5 x 8192 x 2048 int8
-// gated 11.5 / 13.4 / 13.3 (the registers spill), 1 x 11008 x 4096 int4 gated
-// 21.4 / 25.1 / 23.7; three or four CTAs to an SM were slower throughout.
+// 2 / 3 / 4): 1 x 32000 x 4096 bf16 45.7 / 43.6 / 43.0, 5 x 8192 x 2048 int8
+// gated 9.3 / 11.2 / 9.9, 1 x 11008 x 4096 int4 gated 19.3 / 21.7 / 22.7 (the
+// registers of codes spill at 3 and 4); three or four CTAs to an SM were slower
+// throughout.  The 3 of bf16 with 9 to 16 tokens is not the best of them: 13 x
+// 11008 x 4096 20.7 / 26.5 / 27.4.
 template <int QUANT, int T8>
 struct SkinnyCfg {
     static constexpr int KL = QUANT == AMK_QUANT_BF16 ? 8 : QUANT == AMK_QUANT_W8A16 ? 16 : 32;

@@ -52,7 +52,9 @@ __device__ __forceinline__ const float *row_ptr(const VerifyParams &p, int r)
     return r <= p.d ? p.target + r * p.ts : p.draft + (r - p.d - 1) * p.ds;
 }
 
-// exp(y) for y <= 0: y = (n / 64) ln 2 + r with |r| <= ln 2 / 128, so that
+// exp(y) for y <= 0 by a table and a short series (Tang, Table-driven
+// implementation of the exponential function in IEEE floating-point arithmetic,
+// 1989): y = (n / 64) ln 2 + r with |r| <= ln 2 / 128, so that
 // exp(y) = 2^(n >> 6) 2^((n & 63) / 64) exp(r), the second from a table and the
 // last by its series up to r^5 (the next term is below 2^-54).  ln 2 / 64 in
 // two parts keeps r exact.  Half the operations of a general exp.

@@ -126,8 +126,8 @@ def linear(x, w, *, scale=None, bias=None, act: str = "none", up=None, up_scale=
     uint8 [n, k / 2] with scale fp16 [n, ceil(k / 128)] -- contiguous, both of
     one format.  Biases: bf16 [n].  act: "none", "silu", "gelu" or "relu".
     residual: bf16 or fp32 [..., n].  Returns bf16 or fp32 [..., n]: ``out``
-    (which may be ``residual``), else a new tensor of ``out_dtype`` (default:
-    bf16)."""
+    (which may be ``residual`` itself, and overlaps no input otherwise), else a
+    new tensor of ``out_dtype`` (default: bf16)."""
     if _torch is None:
         _load()
     torch = _torch
@@ -220,7 +220,7 @@ def attention(q, k, v, pos: int, *, window: int = 0, sinks: int = 0,
     amk_attention.  ``window`` > 0 limits a token to the last ``window`` rows
     up to its own, and to the first ``sinks`` rows.  scale: default
     1 / sqrt(head_dim).  Returns bf16 [tokens, heads, head_dim] (``out`` if
-    given).  Leading dimensions may be strided; head_dim is contiguous."""
+    given, which overlaps no input).  Leading dimensions may be strided; head_dim is contiguous."""
     if _torch is None:
         _load()
     if scale is None:
@@ -267,8 +267,8 @@ def verify_draft(target_logits, draft_tokens, u, *, draft_logits=None, temperatu
     draft_tokens: int32 [drafts]; u: fp32 [drafts + 1] in [0, 1);
     draft_logits: fp32 [drafts, vocab], or None when the draft has no
     distribution.  temperature: 0 (greedy), or 1e-6 .. 1e6.  Returns (tokens int32
-    [drafts + 1], n_accepted int32 [1]) on the device: the accepted tokens, the
-    drawn one, then -1.  With no drafts it samples one token."""
+    [drafts + 1], n_accepted int32 [1]) on the device (those given, which overlap
+    no input, or new ones): the accepted tokens, the drawn one, then -1.  With no drafts it samples one token."""
     if _torch is None:
         _load()
     torch = _torch
